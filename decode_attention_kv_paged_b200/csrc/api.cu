@@ -9,6 +9,7 @@
 #include <thread>
 
 #include "attn_decode.h"
+#include "fp8_block.cuh"
 #include "gqa_launch.cuh"
 #include "gqa_tc.cuh"
 #include "host_state.cuh"
@@ -667,6 +668,164 @@ int kv_append_mla(const void *latent_new, void *latent_cache, const int32_t *pos
     p.B = B; p.H_kv = 1; p.chunks_per_row = (d_c + d_r) * 2 / 16;
     p.max_blocks = max_blocks_per_seq; p.num_blocks = num_blocks;
     return cuda_status(launch_kv_append(p, (cudaStream_t)stream));
+}
+
+// ------------------------------------------------ block-scaled fp8 cache
+
+static bool valid_fp8_dim(int d) { return d == 64 || d == 128 || d == 256; }
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Fills the run part that append and read share; ATTN_OK or why not.
+static int check_run(const int32_t *positions, const int32_t *offsets, const int32_t *block_table,
+                     int B, int n_tokens, int H_kv, int d, int max_blocks_per_seq, int num_blocks,
+                     int dtype, const attn_visibility *visibility, KvRunParams *run) {
+    if (!positions || !block_table || !aligned4(positions) || !aligned4(offsets) ||
+        !aligned4(block_table))
+        return ATTN_ERR_ARG;
+    if (B <= 0 || n_tokens < 0 || H_kv <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
+        return ATTN_ERR_ARG;
+    if (!offsets && n_tokens != B) return ATTN_ERR_ARG;
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return ATTN_ERR_ARG;
+    if (!valid_fp8_dim(d) || H_kv > 65535 || B > (1 << 29)) return ATTN_ERR_UNSUPPORTED;
+    Visibility vis{0, 0, 0};
+    if (visibility) {
+        const int rc = check_visibility(visibility, max_blocks_per_seq, &vis);
+        if (rc) return rc;
+    }
+    *run = KvRunParams{positions, offsets, block_table, nullptr, B, n_tokens, H_kv,
+                       max_blocks_per_seq, num_blocks, vis};
+    return ATTN_OK;
+}
+
+int kv_append_fp8_block(const void *k_new, const void *v_new, int64_t k_stride, int64_t v_stride,
+                        void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                        const int32_t *positions, const int32_t *offsets,
+                        const int32_t *block_table, int B, int n_tokens, int H_kv, int d,
+                        int max_blocks_per_seq, int num_blocks, int dtype,
+                        const attn_visibility *visibility, void *stream) {
+    if (!k_new || !v_new || !k_cache || !v_cache || !k_scale || !v_scale) return ATTN_ERR_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned4(k_scale) || !aligned4(v_scale))
+        return ATTN_ERR_ARG;
+    KvAppendBlockParams p{};
+    int rc = check_run(positions, offsets, block_table, B, n_tokens, H_kv, d, max_blocks_per_seq,
+                       num_blocks, dtype, visibility, &p.run);
+    if (rc) return rc;
+    const int64_t chunk = dtype == ATTN_BF16 ? 8 : 4, row = (int64_t)H_kv * d;
+    if (k_stride < row || v_stride < row || k_stride % chunk || v_stride % chunk)
+        return ATTN_ERR_ARG;
+    if (n_tokens == 0) return ATTN_OK;
+    DeviceState *st;
+    rc = device_state(&st);
+    if (rc) return rc;
+    p.run.err = st->err;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.k_cache = static_cast<uint8_t *>(k_cache);
+    p.v_cache = static_cast<uint8_t *>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    return cuda_status(
+        launch_kv_append_fp8_block(p, d, dtype == ATTN_BF16, (cudaStream_t)stream));
+}
+
+int kv_read_fp8_block(const void *k_cache, const void *v_cache, const float *k_scale,
+                      const float *v_scale, const int32_t *positions, const int32_t *offsets,
+                      const int32_t *block_table, void *k_out, void *v_out, int B, int n_tokens,
+                      int H_kv, int d, int max_blocks_per_seq, int num_blocks, int dtype,
+                      const attn_visibility *visibility, void *stream) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale || !k_out || !v_out) return ATTN_ERR_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) ||
+        !aligned4(k_scale) || !aligned4(v_scale))
+        return ATTN_ERR_ARG;
+    KvReadBlockParams p{};
+    int rc = check_run(positions, offsets, block_table, B, n_tokens, H_kv, d, max_blocks_per_seq,
+                       num_blocks, dtype, visibility, &p.run);
+    if (rc) return rc;
+    if (n_tokens == 0) return ATTN_OK;
+    DeviceState *st;
+    rc = device_state(&st);
+    if (rc) return rc;
+    p.run.err = st->err;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    return cuda_status(launch_kv_read_fp8_block(p, d, dtype == ATTN_BF16, (cudaStream_t)stream));
+}
+
+// Sizes that both the decode and its workspace query refuse.
+static int check_fp8_block_sizes(int B, int q_len, int H_q, int H_kv, int d) {
+    if (B <= 0 || q_len <= 0 || H_q <= 0 || H_kv <= 0 || H_q % H_kv) return ATTN_ERR_ARG;
+    if (!valid_fp8_dim(d)) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)B * q_len > (1ll << 30) / H_q) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+int64_t attn_decode_gqa_fp8_block_workspace(int B, int q_len, int H_q, int H_kv, int d) {
+    const int rc = check_fp8_block_sizes(B, q_len, H_q, H_kv, d);
+    if (rc) return rc;
+    return 256;
+}
+
+int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cache,
+                              const void *v_cache, const float *k_scale, const float *v_scale,
+                              const int32_t *seq_lens, const int32_t *block_table, void *out,
+                              int B, int q_len, int H_q, int H_kv, int d, float scale,
+                              const attn_visibility *visibility, void *workspace,
+                              int64_t workspace_bytes, void *stream, int max_blocks_per_seq,
+                              int num_blocks) {
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !seq_lens || !block_table || !out ||
+        !workspace)
+        return ATTN_ERR_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+        !aligned4(k_scale) || !aligned4(v_scale) || !aligned4(seq_lens) ||
+        !aligned4(block_table) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return ATTN_ERR_ARG;
+    if (max_blocks_per_seq <= 0 || num_blocks <= 0 || !std::isfinite(scale)) return ATTN_ERR_ARG;
+    int rc = check_fp8_block_sizes(B, q_len, H_q, H_kv, d);
+    if (rc) return rc;
+    if (q_stride < (int64_t)H_q * d || q_stride % 8) return ATTN_ERR_ARG;
+    if ((long long)max_blocks_per_seq * kBlockSize > (1ll << 30)) return ATTN_ERR_ARG;
+    // TMA row coordinates are 32-bit.
+    if ((long long)num_blocks * H_kv > ((1ll << 31) - 128) / kBlockSize) return ATTN_ERR_UNSUPPORTED;
+    Visibility vis{0, 0, 0};
+    if (visibility) {
+        rc = check_visibility(visibility, max_blocks_per_seq, &vis);
+        if (rc) return rc;
+        if (vis.n_g > 0 && q_len > 1) return ATTN_ERR_UNSUPPORTED;
+        if (vis.ring > 0 &&
+            (long long)vis.ring * kBlockSize < (long long)vis.window + q_len - 1 + kBlockSize - 1)
+            return ATTN_ERR_ARG;
+        if (vis.window > (1 << 30)) vis.window = 1 << 30;   // longer than any sequence
+    }
+    const int64_t need = attn_decode_gqa_fp8_block_workspace(B, q_len, H_q, H_kv, d);
+    if (need < 0) return (int)need;
+    if (workspace_bytes < need) return ATTN_ERR_ARG;
+    DeviceState *st;
+    rc = device_state(&st);
+    if (rc) return rc;
+    GqaFp8BlockParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.q_stride = q_stride;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.seq_lens = seq_lens;
+    p.block_table = block_table;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.err = st->err;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.B = B; p.q_len = q_len; p.H_q = H_q; p.H_kv = H_kv; p.group = H_q / H_kv;
+    p.max_blocks = max_blocks_per_seq; p.num_blocks = num_blocks;
+    p.vis = vis;
+    return cuda_status(launch_gqa_fp8_block(p, d, (cudaStream_t)stream));
 }
 
 int attn_decode_plan(const int32_t *seq_lens, int B, int units_per_seq, int window,

@@ -1,0 +1,54 @@
+// fp8_block.cuh -- the block-scaled fp8 cache: E4M3 codes [num_blocks][H_kv]
+// [64][d] with one fp32 scale per (block, head); parameters and launches of
+// its append, read-back and decode kernels.
+#pragma once
+
+#include "plan.cuh"
+
+namespace attn {
+
+struct KvRunParams {
+    const int32_t *positions;     // [B] first position of sequence b's run
+    const int32_t *offsets;       // [B + 1] rows of sequence b, or null: row b
+    const int32_t *block_table;
+    unsigned *err;
+    int B, n_tokens, H_kv, max_blocks, num_blocks;
+    Visibility vis;
+};
+
+struct KvAppendBlockParams {
+    KvRunParams run;
+    const void *k_new, *v_new;    // [n_tokens][H_kv][d], rows k_stride / v_stride apart
+    int64_t k_stride, v_stride;   // elements
+    uint8_t *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+};
+
+struct KvReadBlockParams {
+    KvRunParams run;
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    void *k_out, *v_out;          // [n_tokens][H_kv][d]
+};
+
+cudaError_t launch_kv_append_fp8_block(const KvAppendBlockParams &p, int d, bool bf16,
+                                       cudaStream_t stream);
+cudaError_t launch_kv_read_fp8_block(const KvReadBlockParams &p, int d, bool bf16,
+                                     cudaStream_t stream);
+
+struct GqaFp8BlockParams {
+    const __nv_bfloat16 *q;       // [B][q_len][H_q][d], q_stride elements between positions
+    int64_t q_stride;
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    const int32_t *seq_lens, *block_table;
+    __nv_bfloat16 *out;           // [B][q_len][H_q][d]
+    unsigned *err;
+    float scale_log2;             // softmax scale x log2(e)
+    int B, q_len, H_q, H_kv, group, max_blocks, num_blocks;
+    Visibility vis;               // of a single query; the kernels widen the window by q_len - 1
+};
+
+cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &p, int d, cudaStream_t stream);
+
+}  // namespace attn

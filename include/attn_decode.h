@@ -419,6 +419,102 @@ int attn_mla_absorb_q(const void *q_c, const void *u_k, void *q_latent, int B, i
 int attn_mla_project_out(const void *z, const void *u_v, void *o, int B, int H, int d_c,
                          int d_v, void *stream);
 
+/*
+ * The block-scaled fp8 cache.  k_cache / v_cache [num_blocks][H_kv][64][d]
+ * hold OCP FP8 E4M3 codes; k_scale / v_scale [num_blocks][H_kv] hold ONE fp32
+ * scale for the 64 rows of a block and head, so the key/value used is
+ * code_value * block scale.  Against the per-row scales of kv_append_fp8 it
+ * keeps 1/64 of the scales and lets the decode feed the codes to the tensor
+ * cores as they are.  The scale is a power of two (0 for a block of zeros),
+ * so it costs no relative precision and a block that grows changes the
+ * exponent of its codes only.  d in {64, 128, 256}.
+ *
+ * kv_append_fp8_block -- quantise and write runs of new K and V rows: a
+ * prompt, a chunk of one, or the token of a decode step.  Sequence b's rows
+ * are rows [offsets[b], offsets[b+1]) of k_new / v_new and go to positions
+ * positions[b], positions[b] + 1, ... (through the table mapping of
+ * `visibility`, which may be null).  offsets null: row b belongs to sequence
+ * b (n_tokens = B).
+ *   scale:  need = the smallest power of two s >= 2^-126 with amax <= 448 s,
+ *           amax = max |x| over the block's new finite values (0 if that is
+ *           0).  A block whose row 0 is written starts afresh with s = need;
+ *           a block begun earlier takes s = max(old scale, need), and where
+ *           that grows its earlier rows' codes become RNE(code * old / s).
+ *   codes:  RNE(x / s), saturated to +-448 (infinities too); a NaN stays NaN.
+ * Rows of a block behind the written ones are left as they were.  Where a run
+ * is longer than a ring table, the blocks that a later block of the same run
+ * replaces are not written.  A block may be written by one sequence of a call
+ * only (no order between two), and scales found in the cache must be 0 or
+ * powers of two of at least 2^-126.
+ * k_new, v_new [n_tokens][H_kv][d], bf16 or fp32 (dtype), 16-byte aligned;
+ * k_stride / v_stride: elements from one token's row to the next (at least
+ * H_kv * d, a multiple of 8 (bf16) or 4 (fp32)): rows may be columns of a
+ * fused projection.  Rows whose position or block id is out of range are
+ * skipped and flagged (ATTN_ERR_BAD_BLOCK); offsets that decrease or leave
+ * [0, n_tokens] flag ATTN_ERR_BAD_SEQLEN, and those rows are skipped.
+ * Allocates nothing.
+ */
+int kv_append_fp8_block(const void *k_new, const void *v_new, int64_t k_stride, int64_t v_stride,
+                        void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                        const int32_t *positions, const int32_t *offsets,
+                        const int32_t *block_table, int B, int n_tokens, int H_kv, int d,
+                        int max_blocks_per_seq, int num_blocks, int dtype,
+                        const attn_visibility *visibility, void *stream);
+
+/*
+ * kv_read_fp8_block -- read cached rows back: row offsets[b] + t of k_out /
+ * v_out [n_tokens][H_kv][d] (bf16 or fp32, contiguous, 16-byte aligned) gets
+ * code_value * block scale, rounded to nearest even, of position positions[b]
+ * + t of sequence b (for prefix reuse by a dense prefill, cache migration,
+ * checks).  Arguments as for kv_append_fp8_block.  Positions that the table
+ * row cannot name, whose block id is outside the pool, or whose ring slot a
+ * later position of the same run holds, read as zeros and are flagged
+ * (ATTN_ERR_BAD_BLOCK).  Output rows that belong to no sequence are left as
+ * they were.  Allocates nothing.
+ */
+int kv_read_fp8_block(const void *k_cache, const void *v_cache, const float *k_scale,
+                      const float *v_scale, const int32_t *positions, const int32_t *offsets,
+                      const int32_t *block_table, void *k_out, void *v_out, int B, int n_tokens,
+                      int H_kv, int d, int max_blocks_per_seq, int num_blocks, int dtype,
+                      const attn_visibility *visibility, void *stream);
+
+/*
+ * attn_decode_gqa_fp8_block -- decode attention over the block-scaled fp8
+ * cache, for one or several query positions of every sequence: query i of
+ * q_len sits at position T_b - q_len + i and sees keys up to its own position
+ * (q_len = 1: the decode step; q_len > 1: drafted tokens being verified,
+ * their K/V appended first).  `visibility` (may be null) as for
+ * attn_decode_gqa_ext, applied to each query's own position; a global set
+ * needs q_len = 1 (ATTN_ERR_UNSUPPORTED), a ring ring_blocks * 64 >= window +
+ * q_len + 62.  A query that sees no key (T_b < q_len - i) gets a zero row.
+ * q [B][q_len][H_q][d] bf16, q_stride elements (>= H_q * d, a multiple of 8)
+ * from one position's heads to the next; out [B][q_len][H_q][d] bf16,
+ * contiguous; scale finite.  Scales in the cache: 0, or positive and within
+ * [2^-64, 2^64] for full precision; a block's scale of 0 makes its values 0
+ * (not its weight).  Codes in rows that no query of the sequence sees may
+ * be anything, NaN included; a NaN in a row that one query of the sequence
+ * sees may reach that sequence's other queries.
+ * workspace: device memory of at least attn_decode_gqa_fp8_block_workspace
+ * bytes, 256-byte aligned, which nothing else uses until the call's work is
+ * done (a captured graph keeps its own); its contents need no preparation.
+ * ATTN_ERR_ARG if it is too small.  Allocates nothing.  Other errors as
+ * attn_decode_gqa_ext.
+ */
+int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cache,
+                              const void *v_cache, const float *k_scale, const float *v_scale,
+                              const int32_t *seq_lens, const int32_t *block_table, void *out,
+                              int B, int q_len, int H_q, int H_kv, int d, float scale,
+                              const attn_visibility *visibility, void *workspace,
+                              int64_t workspace_bytes, void *stream, int max_blocks_per_seq,
+                              int num_blocks);
+
+/*
+ * attn_decode_gqa_fp8_block_workspace -- bytes of workspace that
+ * attn_decode_gqa_fp8_block needs on the current device for these sizes, or a
+ * negative attn_status.
+ */
+int64_t attn_decode_gqa_fp8_block_workspace(int B, int q_len, int H_q, int H_kv, int d);
+
 /* Human-readable name of a status code (static storage). */
 const char *attn_status_string(int status);
 
