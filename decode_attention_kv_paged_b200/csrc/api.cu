@@ -768,9 +768,13 @@ static int check_fp8_block_sizes(int B, int q_len, int H_q, int H_kv, int d) {
 }
 
 int64_t attn_decode_gqa_fp8_block_workspace(int B, int q_len, int H_q, int H_kv, int d) {
-    const int rc = check_fp8_block_sizes(B, q_len, H_q, H_kv, d);
+    int rc = check_fp8_block_sizes(B, q_len, H_q, H_kv, d);
     if (rc) return rc;
-    return 256;
+    DeviceState *st;
+    rc = device_state(&st);
+    if (rc) return rc;
+    const int ctas = tl_num_ctas > 0 ? tl_num_ctas : st->num_sms;
+    return fp8_block_workspace_bytes(ctas, q_len * (H_q / H_kv), d);
 }
 
 int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cache,
@@ -804,13 +808,14 @@ int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cac
             return ATTN_ERR_ARG;
         if (vis.window > (1 << 30)) vis.window = 1 << 30;   // longer than any sequence
     }
-    const int64_t need = attn_decode_gqa_fp8_block_workspace(B, q_len, H_q, H_kv, d);
-    if (need < 0) return (int)need;
-    if (workspace_bytes < need) return ATTN_ERR_ARG;
+    if (workspace_bytes <= 0) return ATTN_ERR_ARG;
     DeviceState *st;
     rc = device_state(&st);
     if (rc) return rc;
     GqaFp8BlockParams p{};
+    p.num_ctas = tl_num_ctas > 0 ? tl_num_ctas : st->num_sms;
+    if (workspace_bytes < fp8_block_workspace_bytes(p.num_ctas, q_len * (H_q / H_kv), d))
+        return ATTN_ERR_ARG;
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.q_stride = q_stride;
     p.k_cache = static_cast<const uint8_t *>(k_cache);
@@ -825,7 +830,8 @@ int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cac
     p.B = B; p.q_len = q_len; p.H_q = H_q; p.H_kv = H_kv; p.group = H_q / H_kv;
     p.max_blocks = max_blocks_per_seq; p.num_blocks = num_blocks;
     p.vis = vis;
-    return cuda_status(launch_gqa_fp8_block(p, d, (cudaStream_t)stream));
+    p.timeout_ns = kDefaultTimeoutNs;
+    return cuda_status(launch_gqa_fp8_block(p, d, workspace, (cudaStream_t)stream));
 }
 
 int attn_decode_plan(const int32_t *seq_lens, int B, int units_per_seq, int window,

@@ -47,8 +47,20 @@ struct GqaFp8BlockParams {
     float scale_log2;             // softmax scale x log2(e)
     int B, q_len, H_q, H_kv, group, max_blocks, num_blocks;
     Visibility vis;               // of a single query; the kernels widen the window by q_len - 1
+    int num_ctas;
+    unsigned long long timeout_ns;
+    // filled by the launch: the query rows of a K/V head (group x q_len) in
+    // chunks of chunk_rows; partials [2 num_ctas][columns][d] with their
+    // reference and sum
+    int chunk_rows, chunks;
+    float *ws_o;
+    float2 *ws_ml;
 };
 
-cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &p, int d, cudaStream_t stream);
+// Workspace of a launch over num_ctas CTAs with `rows` query rows per K/V head.
+int64_t fp8_block_workspace_bytes(int num_ctas, int rows, int d);
+
+cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &p, int d, void *workspace,
+                                 cudaStream_t stream);
 
 }  // namespace attn
