@@ -7,6 +7,7 @@ the current CUDA stream, and raises AttnError on a failing status.  There is
 no fallback: if the library is missing, ``load()`` raises.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -104,7 +105,7 @@ def load():
             fn.restype = ctypes.c_int
     n, vis = ctypes.c_int64, ctypes.POINTER(Visibility)
     lib.kv_append_fp8_block.argtypes = [p] * 2 + [n] * 2 + [p] * 7 + [i] * 7 + [vis, p]
-    lib.kv_read_fp8_block.argtypes = [p] * 9 + [i] * 7 + [vis, p]
+    lib.kv_read_fp8_block.argtypes = [p] * 9 + [i] * 8 + [vis, p]
     lib.attn_decode_gqa_fp8_block.argtypes = ([p, n] + [p] * 7 + [i] * 5 +
                                               [f, vis, p, n, p, i, i])
     lib.attn_decode_gqa_fp8_block_workspace.argtypes = [i] * 5
@@ -407,94 +408,119 @@ def kv_append_mla(latent_new, latent_cache, positions, block_table, d_c=512,
 
 # --------------------------------------------------- block-scaled fp8 cache
 
-class _On:
-    """One call's device: checks that every tensor lies on it, makes it current
-    and names the stream (the device's current one unless given)."""
+# These calls are a step's smallest, so their checks are kept short: one
+# comparison per property, no tensor or stream objects made on the way.
 
-    def __init__(self, first, stream):
-        if not isinstance(first, torch.Tensor) or first.device.type != "cuda":
-            raise ValueError("the tensors must be CUDA tensors")
-        self.device = first.device
-        self.stream = stream
-        self.before = None
+def _at(t, name, dtype, dev, shape=None, dense=True):
+    """Address of a tensor of a call on device `dev`, checked."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    def __enter__(self):
-        index = self.device.index
-        if torch.cuda.current_device() != index:
-            self.before = torch.cuda.current_device()
-            torch.cuda.set_device(index)
-        if self.stream is None:
-            self.stream = torch.cuda.current_stream()
-        elif self.stream.device_index != index:
-            self.__exit__()
+
+def _device_of(t, name):
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _on_device(call):
+    """Runs `call(dev, stream handle, ...)` on the device of its first argument
+    and the given stream (else that device's current one)."""
+    @functools.wraps(call)
+    def run(first, *args, stream=None, **kwargs):
+        dev = _device_of(first, call.__code__.co_varnames[2])
+        if stream is None:
+            handle = torch._C._cuda_getCurrentRawStream(dev)
+        elif stream.device_index == dev:
+            handle = stream.cuda_stream
+            with torch.cuda.stream(stream):          # what the call allocates is the stream's
+                return call(dev, handle, first, *args, **kwargs)
+        else:
             raise ValueError("the stream belongs to another device than the tensors")
-        return self
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
-        return False
-
-    def ptr(self, t, name, dtype, shape=None, dense=True):
-        """Address of a tensor of this call (None stays None)."""
-        if t is None:
-            return None
-        if not isinstance(t, torch.Tensor) or t.device != self.device:
-            raise ValueError(f"{name} must be a tensor on {self.device}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if shape is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if dense and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
+        if torch._C._cuda_getDevice() != dev:
+            with torch.cuda.device(dev):
+                return call(dev, handle, first, *args, **kwargs)
+        return call(dev, handle, first, *args, **kwargs)
+    return run
 
 
-def _block_cache(on, k_cache, v_cache, k_scale, v_scale):
+def _block_cache(dev, k_cache, v_cache, k_scale, v_scale):
     """Addresses and sizes of a block-scaled cache."""
-    if k_cache.dim() != 4 or k_cache.shape[2] != BLOCK_SIZE:
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != BLOCK_SIZE:
         raise ValueError("cache must be [num_blocks][H_kv][64][d] for K and V")
-    nblk, H_kv, _, d = shape = tuple(k_cache.shape)
-    at = (on.ptr(k_cache, "k_cache", torch.uint8, shape),
-          on.ptr(v_cache, "v_cache", torch.uint8, shape),
-          on.ptr(k_scale, "k_scale", torch.float32, (nblk, H_kv)),
-          on.ptr(v_scale, "v_scale", torch.float32, (nblk, H_kv)))
-    return at, nblk, H_kv, d
+    scales, u8, f32 = shape[:2], torch.uint8, torch.float32
+    return (_at(k_cache, "k_cache", u8, dev), _at(v_cache, "v_cache", u8, dev, shape),
+            _at(k_scale, "k_scale", f32, dev, scales),
+            _at(v_scale, "v_scale", f32, dev, scales)), shape[0], shape[1], shape[3]
 
 
-def _run_of(on, positions, block_table, offsets, n_tokens):
+def _run_of(dev, positions, block_table, offsets, n_tokens):
     """Addresses and sizes of the token runs of an append or a read."""
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B][max_blocks]")
     B, width = block_table.shape
-    if offsets is None and n_tokens != B:
+    i32 = torch.int32
+    if offsets is not None:
+        offsets = _at(offsets, "offsets", i32, dev, (B + 1,))
+    elif n_tokens != B:
         raise ValueError("without offsets there is one row a sequence")
-    at = (on.ptr(positions, "positions", torch.int32, (B,)),
-          on.ptr(offsets, "offsets", torch.int32, (B + 1,)),
-          on.ptr(block_table, "block_table", torch.int32))
-    return at, B, width
+    return (_at(positions, "positions", i32, dev, (B,)), offsets,
+            _at(block_table, "block_table", i32, dev)), B, width
 
 
-def _vis_on(on, window, sink_tokens, ring_blocks, global_pos, B):
+def _vis_on(dev, window, sink_tokens, ring_blocks, global_pos, B):
     if global_pos is None:
         if window <= 0 and sink_tokens == 0 and ring_blocks == 0:
             return None
-    elif global_pos.dim() != 2 or global_pos.shape[0] != B:
+        return ctypes.byref(Visibility(int(window), int(sink_tokens), int(ring_blocks), None, 0))
+    if global_pos.dim() != 2 or global_pos.shape[0] != B:
         raise ValueError("global_pos must be [B][n_global]")
-    at = on.ptr(global_pos, "global_pos", torch.int32)
+    at = _at(global_pos, "global_pos", torch.int32, dev)
     return ctypes.byref(Visibility(int(window), int(sink_tokens), int(ring_blocks), at,
-                                   0 if at is None else int(global_pos.shape[1])))
+                                   int(global_pos.shape[1])))
 
 
-def _rows_of(on, t, name, dtype, tail):
+def _rows_of(dev, t, name, dtype, tail):
     """Address and row stride of [rows]... whose rows are dense but may lie apart."""
-    at = on.ptr(t, name, dtype, dense=False)
-    if tuple(t.shape[1:]) != tail:
+    if t.shape[1:] != tail:
         raise ValueError(f"{name} must be [tokens]{list(tail)}, got {list(t.shape)}")
-    if t.numel() and not t[0].is_contiguous():
+    at = _at(t, name, dtype, dev, dense=False)
+    if t.is_contiguous():
+        return at, tail[0] * tail[1]
+    row = t.stride()
+    if row[2] != 1 and tail[1] > 1 or row[1] != tail[1] and tail[0] > 1:
         raise ValueError(f"each row of {name} must be contiguous")
     # the stride of a single row says nothing
-    return at, t.stride(0) if t.shape[0] > 1 else tail[0] * tail[1]
+    return at, row[0] if t.shape[0] > 1 else tail[0] * tail[1]
+
+
+@_on_device
+def _append_fp8_block(dev, stream, k_new, v_new, k_cache, v_cache, k_scale, v_scale, positions,
+                      block_table, offsets, window, sink_tokens, ring_blocks, global_pos):
+    (kc, vc, ks, vs), nblk, H_kv, d = _block_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    n, dt, tail = k_new.shape[0], k_new.dtype, (H_kv, d)
+    code = _dtype_code(dt)
+    kn, k_stride = _rows_of(dev, k_new, "k_new", dt, tail)
+    vn, v_stride = _rows_of(dev, v_new, "v_new", dt, tail)
+    if v_new.shape[0] != n:
+        raise ValueError("k_new and v_new must have as many rows")
+    (pos, off, tab), B, width = _run_of(dev, positions, block_table, offsets, n)
+    vis = _vis_on(dev, window, sink_tokens, ring_blocks, global_pos, B)
+    if n == 0:
+        return
+    rc = load().kv_append_fp8_block(kn, vn, k_stride, v_stride, kc, vc, ks, vs, pos, off, tab, B,
+                                    n, H_kv, d, width, nblk, code, vis, stream)
+    if rc:
+        _check(rc, "kv_append_fp8_block")
 
 
 def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, positions, block_table,
@@ -510,23 +536,34 @@ def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, positi
     b's.  A block whose first row is written takes the scale its rows ask for;
     a block begun earlier keeps its scale or grows it, its codes rounded to the
     new one."""
-    with _On(k_cache, stream) as on:
-        (kc, vc, ks, vs), nblk, H_kv, d = _block_cache(on, k_cache, v_cache, k_scale, v_scale)
-        n = k_new.shape[0]
-        dt = k_new.dtype
-        code = _dtype_code(dt)
-        kn, k_stride = _rows_of(on, k_new, "k_new", dt, (H_kv, d))
-        vn, v_stride = _rows_of(on, v_new, "v_new", dt, (H_kv, d))
-        if v_new.shape[0] != n:
-            raise ValueError("k_new and v_new must have as many rows")
-        (pos, off, tab), B, width = _run_of(on, positions, block_table, offsets, n)
-        vis = _vis_on(on, window, sink_tokens, ring_blocks, global_pos, B)
-        if n == 0:
-            return
-        rc = load().kv_append_fp8_block(kn, vn, k_stride, v_stride, kc, vc, ks, vs, pos, off, tab,
-                                        B, n, H_kv, d, width, nblk, code, vis,
-                                        on.stream.cuda_stream)
-        _check(rc, "kv_append_fp8_block")
+    _append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, positions, block_table,
+                      offsets, window, sink_tokens, ring_blocks, global_pos, stream=stream)
+
+
+@_on_device
+def _read_fp8_block(dev, stream, k_cache, v_cache, k_scale, v_scale, positions, block_table,
+                    n, offsets, dtype, out, window, sink_tokens, ring_blocks, global_pos):
+    (kc, vc, ks, vs), nblk, H_kv, d = _block_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    code = _dtype_code(dtype)
+    (pos, off, tab), B, width = _run_of(dev, positions, block_table, offsets, n)
+    vis = _vis_on(dev, window, sink_tokens, ring_blocks, global_pos, B)
+    shape = (n, H_kv, d)
+    # rows that no sequence owns are zeros in new tensors
+    rest = 1 if out is None else 0
+    if out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        v_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        ko, vo = k_out.data_ptr(), v_out.data_ptr()
+    else:
+        k_out, v_out = out
+        ko = _at(k_out, "k_out", dtype, dev, shape)
+        vo = _at(v_out, "v_out", dtype, dev, shape)
+    if n:
+        rc = load().kv_read_fp8_block(kc, vc, ks, vs, pos, off, tab, ko, vo, B, n, H_kv, d, width,
+                                      nblk, code, rest, vis, stream)
+        if rc:
+            _check(rc, "kv_read_fp8_block")
+    return k_out, v_out
 
 
 def kv_read_fp8_block(k_cache, v_cache, k_scale, v_scale, positions, block_table, n_tokens,
@@ -535,47 +572,73 @@ def kv_read_fp8_block(k_cache, v_cache, k_scale, v_scale, positions, block_table
     """(k, v) [n_tokens][H_kv][d]: cached rows read back, code value times block
     scale rounded to `dtype` (bf16 or fp32).  Row offsets[b] + t is position
     positions[b] + t of sequence b; without offsets row b is positions[b].
-    `out`: a pair to write into; rows behind offsets[B] are left as they were."""
-    with _On(k_cache, stream) as on:
-        (kc, vc, ks, vs), nblk, H_kv, d = _block_cache(on, k_cache, v_cache, k_scale, v_scale)
-        n = int(n_tokens)
-        code = _dtype_code(dtype)
-        if out is None:
-            # rows that no sequence owns are zeros in a new tensor
-            make = torch.empty if offsets is None else torch.zeros
-            with torch.cuda.stream(on.stream):
-                out = tuple(make((n, H_kv, d), dtype=dtype, device=on.device) for _ in range(2))
-        k_out, v_out = out
-        (pos, off, tab), B, width = _run_of(on, positions, block_table, offsets, n)
-        vis = _vis_on(on, window, sink_tokens, ring_blocks, global_pos, B)
-        ko = on.ptr(k_out, "k_out", dtype, (n, H_kv, d))
-        vo = on.ptr(v_out, "v_out", dtype, (n, H_kv, d))
-        if n:
-            rc = load().kv_read_fp8_block(kc, vc, ks, vs, pos, off, tab, ko, vo, B, n, H_kv, d,
-                                          width, nblk, code, vis, on.stream.cuda_stream)
-            _check(rc, "kv_read_fp8_block")
-        return k_out, v_out
+    `out`: a pair to write into, whose rows behind offsets[B] are left as they
+    were; in new tensors they are zeros."""
+    return _read_fp8_block(k_cache, v_cache, k_scale, v_scale, positions, block_table,
+                           int(n_tokens), offsets, dtype, out, window, sink_tokens, ring_blocks,
+                           global_pos, stream=stream)
 
 
 def _block_queries(q):
-    if q.dim() == 3:
-        B, H_q, d = q.shape
-        return B, 1, H_q, d
-    if q.dim() == 4:
-        return tuple(q.shape)
-    raise ValueError("q must be [B][H_q][d] or [B][q_len][H_q][d]")
+    """(B, q_len, H_q, d, stride between positions) of the queries."""
+    shape = q.shape
+    if len(shape) == 3:
+        B, H_q, d = shape
+        L = 1
+    elif len(shape) == 4:
+        B, L, H_q, d = shape
+    else:
+        raise ValueError("q must be [B][H_q][d] or [B][q_len][H_q][d]")
+    if q.is_contiguous():
+        return B, L, H_q, d, H_q * d
+    st = q.stride()
+    # a dimension of one has no stride; a single position takes its sequence's
+    row = st[0] if L == 1 else st[1]
+    if (st[-1] != 1 and d > 1) or (st[-2] != d and H_q > 1) or \
+            (L > 1 and B > 1 and st[0] != L * row):
+        raise ValueError("q must hold each position's heads contiguously, positions evenly apart")
+    return B, L, H_q, d, row if B * L > 1 else H_q * d
 
 
 def fp8_block_workspace(q, k_cache):
     """A workspace for decode_gqa_fp8_block calls with queries and a cache of
     these shapes (for calls that follow one another on one stream; a captured
     graph needs one of its own)."""
-    B, L, H_q, d = _block_queries(q)
+    B, L, H_q, d, _ = _block_queries(q)
     with torch.cuda.device(q.device):
         n = load().attn_decode_gqa_fp8_block_workspace(B, L, H_q, k_cache.shape[1], d)
         if n < 0:
             raise AttnError(n, "attn_decode_gqa_fp8_block_workspace")
         return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+@_on_device
+def _decode_fp8_block(dev, stream, q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table,
+                      scale, window, sink_tokens, ring_blocks, out, global_pos, workspace):
+    (kc, vc, ks, vs), nblk, H_kv, d = _block_cache(dev, k_cache, v_cache, k_scale, v_scale)
+    B, L, H_q, d_q, q_stride = _block_queries(q)
+    if d_q != d:
+        raise ValueError("q and the cache must have the same head dim")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B][max_blocks]")
+    bf, i32, shape = torch.bfloat16, torch.int32, q.shape
+    qp = _at(q, "q", bf, dev, dense=False)
+    lens, tab = _at(seq_lens, "seq_lens", i32, dev, (B,)), _at(block_table, "block_table", i32, dev)
+    vis = _vis_on(dev, window, sink_tokens, ring_blocks, global_pos, B)
+    if workspace is None:
+        workspace = fp8_block_workspace(q, k_cache)
+    wp = _at(workspace, "workspace", torch.uint8, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=bf, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _at(out, "out", bf, dev, shape)
+    rc = load().attn_decode_gqa_fp8_block(qp, q_stride, kc, vc, ks, vs, lens, tab, op, B, L, H_q,
+                                          H_kv, d, scale, vis, wp, workspace.numel(), stream,
+                                          block_table.shape[1], nblk)
+    if rc:
+        _check(rc, "attn_decode_gqa_fp8_block")
+    return out
 
 
 def decode_gqa_fp8_block(q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table, scale,
@@ -588,41 +651,9 @@ def decode_gqa_fp8_block(q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_
     positions or global set (q_len 1 only).  Rows that see nothing are zero.
     `workspace`: from fp8_block_workspace, not shared with a call that may run
     at the same time; without it each call takes a new one."""
-    with _On(q, stream) as on:
-        (kc, vc, ks, vs), nblk, H_kv, d = _block_cache(on, k_cache, v_cache, k_scale, v_scale)
-        B, L, H_q, d_q = _block_queries(q)
-        if d_q != d:
-            raise ValueError("q and the cache must have the same head dim")
-        if block_table.dim() != 2 or block_table.shape[0] != B:
-            raise ValueError("block_table must be [B][max_blocks]")
-        bf = torch.bfloat16
-        qp = on.ptr(q, "q", bf, dense=False)
-        q_stride = q.stride(-3) if B * L > 1 else H_q * d
-        if not q.is_contiguous() and (q.stride(-1) != 1 or q.stride(-2) != d or
-                                      (q.dim() == 4 and B > 1 and L > 1 and
-                                       q.stride(0) != L * q_stride)):
-            raise ValueError("q must hold each position's heads contiguously, positions evenly "
-                             "apart")
-        if q.dim() == 4 and L == 1 and B > 1:
-            q_stride = q.stride(0)
-        vis = _vis_on(on, window, sink_tokens, ring_blocks, global_pos, B)
-        need = load().attn_decode_gqa_fp8_block_workspace(B, L, H_q, H_kv, d)
-        if need < 0:
-            raise AttnError(need, "attn_decode_gqa_fp8_block_workspace")
-        if out is None or workspace is None:
-            with torch.cuda.stream(on.stream):
-                if out is None:
-                    out = torch.empty(q.shape, dtype=bf, device=on.device)
-                if workspace is None:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=on.device)
-        rc = load().attn_decode_gqa_fp8_block(
-            qp, q_stride, kc, vc, ks, vs, on.ptr(seq_lens, "seq_lens", torch.int32, (B,)),
-            on.ptr(block_table, "block_table", torch.int32),
-            on.ptr(out, "out", bf, tuple(q.shape)), B, L, H_q, H_kv, d, float(scale), vis,
-            on.ptr(workspace, "workspace", torch.uint8), workspace.numel(),
-            on.stream.cuda_stream, block_table.shape[1], nblk)
-        _check(rc, "attn_decode_gqa_fp8_block")
-        return out
+    return _decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table,
+                             float(scale), window, sink_tokens, ring_blocks, out, global_pos,
+                             workspace, stream=stream)
 
 
 def plan(seq_lens, units_per_seq, window, max_blocks, num_ctas, stream=None):

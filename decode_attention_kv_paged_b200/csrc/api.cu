@@ -736,7 +736,7 @@ int kv_read_fp8_block(const void *k_cache, const void *v_cache, const float *k_s
                       const float *v_scale, const int32_t *positions, const int32_t *offsets,
                       const int32_t *block_table, void *k_out, void *v_out, int B, int n_tokens,
                       int H_kv, int d, int max_blocks_per_seq, int num_blocks, int dtype,
-                      const attn_visibility *visibility, void *stream) {
+                      int zero_rest, const attn_visibility *visibility, void *stream) {
     if (!k_cache || !v_cache || !k_scale || !v_scale || !k_out || !v_out) return ATTN_ERR_ARG;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) ||
         !aligned4(k_scale) || !aligned4(v_scale))
@@ -756,6 +756,7 @@ int kv_read_fp8_block(const void *k_cache, const void *v_cache, const float *k_s
     p.v_scale = v_scale;
     p.k_out = k_out;
     p.v_out = v_out;
+    p.zero_rest = zero_rest != 0;
     return cuda_status(launch_kv_read_fp8_block(p, d, dtype == ATTN_BF16, (cudaStream_t)stream));
 }
 
@@ -796,6 +797,9 @@ int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cac
     if (rc) return rc;
     if (q_stride < (int64_t)H_q * d || q_stride % 8) return ATTN_ERR_ARG;
     if ((long long)max_blocks_per_seq * kBlockSize > (1ll << 30)) return ATTN_ERR_ARG;
+    // A CTA counts its blocks in 32 bits.
+    if ((double)max_blocks_per_seq * H_q * q_len * (B > 64 ? B / 64 : 1) > 1e9)
+        return ATTN_ERR_UNSUPPORTED;
     // TMA row coordinates are 32-bit.
     if ((long long)num_blocks * H_kv > ((1ll << 31) - 128) / kBlockSize) return ATTN_ERR_UNSUPPORTED;
     Visibility vis{0, 0, 0};

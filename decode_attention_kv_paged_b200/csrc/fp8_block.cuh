@@ -29,12 +29,19 @@ struct KvReadBlockParams {
     const uint8_t *k_cache, *v_cache;
     const float *k_scale, *v_scale;
     void *k_out, *v_out;          // [n_tokens][H_kv][d]
+    bool zero_rest;               // rows that no sequence owns become zeros
 };
 
 cudaError_t launch_kv_append_fp8_block(const KvAppendBlockParams &p, int d, bool bf16,
                                        cudaStream_t stream);
 cudaError_t launch_kv_read_fp8_block(const KvReadBlockParams &p, int d, bool bf16,
                                      cudaStream_t stream);
+
+// A unit cut at the end of a CTA's range: the CTAs that hold it, the first
+// one's partial, sequence and unit; last < first where nothing is cut.
+struct FbCut {
+    int first, last, slot, b, unit;
+};
 
 struct GqaFp8BlockParams {
     const __nv_bfloat16 *q;       // [B][q_len][H_q][d], q_stride elements between positions
@@ -55,6 +62,9 @@ struct GqaFp8BlockParams {
     int chunk_rows, chunks;
     float *ws_o;
     float2 *ws_ml;
+    FbCut *ws_cut;                // [num_ctas]
+    bool whole_units;             // one CTA per unit, nothing split
+    bool small_plan;              // few sequences, a list that 32 bits count
 };
 
 // Workspace of a launch over num_ctas CTAs with `rows` query rows per K/V head.

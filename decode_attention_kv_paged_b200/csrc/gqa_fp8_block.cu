@@ -29,11 +29,13 @@
 // the factor that brings it to the running reference.  Sums of weights stay in
 // fp32 registers, per key lane, until the unit's end.
 //
-// Roles (one CTA per SM, 12 warps): warp 0 loads tiles of two blocks by TMA
+// Roles (one CTA per SM, 16 warps): warp 0 loads tiles of two blocks by TMA
 // (swizzled as the MMA reads them) into two rings, with the block scales;
 // warps 1 and 2 issue the two products; warp 3 prepares the next unit's
-// queries; warps 4-7 are the softmax, warps 8-11 keep the output.  S, P and O
-// are double-buffered.  Every wait is bounded, and tensor memory always freed.
+// queries; warps 4-7 and 8-11 are the softmax, on even and odd tiles (a tile
+// is one long chain of latencies for its four warps, so two are kept going);
+// warps 12-15 keep the output.  S, P and O are double-buffered.  Every wait is
+// bounded, and tensor memory always freed.
 //
 // The work is split over all SMs by visible blocks (plan.cuh); a unit cut by a
 // CTA boundary leaves fp32 partials, which a second kernel, waiting on the
@@ -48,8 +50,9 @@
 
 namespace attn {
 
-constexpr int kFbThreads = 384;
+constexpr int kFbThreads = 512;
 constexpr int kFbMaxStages = 8;
+constexpr int kFbWholeBlocks = 8;                     // see launch_gqa_fp8_block
 constexpr int kFbTile = 2 * kBlockSize;               // keys of a tile
 
 template <int D, int NQ>
@@ -63,7 +66,7 @@ struct FbCfg {
     static constexpr int kSlot = kFbTile * D;
     static constexpr int kQBytes = kN * D;
     static constexpr int kPBytes = kN * kFbTile;
-    static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 8 * 1024 + 1024 /*align*/;
+    static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 10 * 1024 + 1024 /*align*/;
     static constexpr int kSlots = (227 * 1024 - kFixed) / kSlot;
     static constexpr int kKStages = kSlots / 2 > kFbMaxStages ? kFbMaxStages : kSlots / 2;
     static constexpr int kVStages =
@@ -73,39 +76,45 @@ struct FbCfg {
     static constexpr int kOffQ = kOffV + kVStages * kSlot;
     static constexpr int kOffP = kOffQ + 2 * kQBytes;
     static constexpr int kOffBar = kOffP + 2 * kPBytes;
-    static constexpr int kSmem = kOffBar + 8 * 1024 + 1024;
+    static constexpr int kSmem = kOffBar + 10 * 1024 + 1024;
     static constexpr uint32_t kTmemS = 0, kTmemO = 2 * kN;
     static constexpr uint32_t kTmemUsed = 2 * kN + 2 * kHalves * kN;
     static constexpr uint32_t kTmemCols =
         kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+    // With 32 columns the softmax needs more than its even share of registers.
+    static constexpr bool kSplitRegs = NQ == 32;
+    static constexpr int kRegsLoad = 72, kRegsSoftmax = 152, kRegsOutput = 136;
+    static_assert(kRegsLoad + 2 * kRegsSoftmax + kRegsOutput <= 4 * 128, "register split");
     static_assert(kKStages >= 2 && kVStages >= 2, "at least two stages per ring");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 template <int NQ>
 struct FbShared {
+    // In the order of the arrivals that complete them (see their set-up).
     uint64_t k_full[kFbMaxStages], k_empty[kFbMaxStages];
     uint64_t v_full[kFbMaxStages], v_empty[kFbMaxStages];
-    uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], s_free[2];
-    uint64_t p_full[2], o_full[2], o_free[2];
+    uint64_t q_full[2], s_full[2], o_full[2], q_empty[2], s_free[2], p_full[2], o_free[2];
     uint64_t mma_final;
+    static constexpr int kBars = 4 * kFbMaxStages + 15;
     // Per V slot and block of the tile: K scale x softmax scale (log2 units),
-    // log2 of the V scale, its reciprocal, whether V counts (scale not 0).
+    // log2 of the V scale, its reciprocal, 0 where the V scale is 0.
     alignas(16) float4 info[kFbMaxStages][2];
-    alignas(16) float qsc[2][NQ];              // power-of-two scale of each query row
-    int row_i[2][NQ];              // query position of each row
-    float wmax[2][4][NQ];          // a tile's largest score per warp
-    alignas(16) float2 ref[4][NQ];             // per warp: the tile's reference - 8, its factor
-    float grow[4][NQ];             // per warp: factor of what was added before
-    alignas(16) float2 join[2][NQ];            // for the output warps: factor of the tile, of the rest
-    float lsum[2][4][NQ];          // at a unit's end: sums of weights per warp
-    float top[2][NQ];              // and the reference they are relative to
+    alignas(16) float qsc[2][NQ];  // power-of-two scale of each query row
+    alignas(16) int row_i[2][NQ];  // query position of each row
+    alignas(16) float wmax[2][4][NQ];   // per softmax group: largest scores per warp
+    alignas(16) float2 ref[8][NQ]; // per softmax warp: reference of the weights, factor in the sum
+    alignas(16) float grow[8][NQ]; // per softmax warp: factor of the sum so far
+    alignas(16) float top[2][NQ];  // a tile's largest score (with its V scale)
+    alignas(16) float2 join[4][NQ];     // per output warp: factor of the tile, of the rest
+    // at a unit's end, per softmax group: sums of weights, what they are relative to
+    float lsum[2][2][4][NQ];
+    float ltop[2][2][NQ];
     uint32_t tmem_base;
     int abort;
     PlanScratch plan;
 };
-static_assert(sizeof(FbShared<32>) <= 8 * 1024, "shared block");
+static_assert(sizeof(FbShared<32>) <= 10 * 1024, "shared block");
 
 // Largest of x over the warp (NaN only where every lane is NaN).
 __device__ __forceinline__ float warp_max(float x) {
@@ -170,23 +179,108 @@ __device__ __forceinline__ void fb_tmem_ld(uint32_t addr, float *v) {
     else tmem_ld16(addr, v);
 }
 
-// The part of the work list that a CTA takes, walked unit by unit.
+// Waits by testing the barrier over and over: for the threads that issue the
+// products, which everything else waits on (a suspended wait wakes up some 200
+// cycles late).  Bounds and results as mbar_wait.
+__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity,
+                                          unsigned long long timeout_ns, unsigned *err,
+                                          volatile int *abort) {
+    unsigned long long t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_test(bar, parity)) return true;
+        if ((it & 15u) == 15u && *abort) return false;
+        if ((it & 1023u) == 1023u) {
+            const unsigned long long now = global_timer_ns();
+            if (t0 == 0) {
+                t0 = now;
+            } else if (now - t0 > timeout_ns) {
+                raise_error(err, kErrTimeout);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// The part of the work list that a CTA takes, walked unit by unit: `len`
+// visible blocks of unit `unit` of sequence b, from its block blk_off on.
 template <bool G>
 struct FbWalk {
-    SegmentWalkerT<G> w;
-    int len;
-    __device__ void init(const PlanArgs &pa, long long lo, long long hi, int seq,
-                         long long base) {
-        w.init(pa, lo, hi, seq, base);
-        len = w.done() ? 0 : w.seg_len();
+    SegmentWalkerT<G> w;      // its block mapping; pos and end are not used
+    int rest, len;            // blocks of the range left, of this unit's part
+
+    __device__ void part() { len = min(rest, w.nb - w.blk_off); }
+    __device__ void init(const PlanArgs &pa, int blocks, int b, long long off) {
+        w.seq_lens = pa.seq_lens;
+        w.B = pa.B;
+        w.units = pa.units_per_seq;
+        w.vis = pa.vis;
+        w.max_blocks = pa.max_blocks;
+        rest = blocks;
+        len = 0;
+        if (rest <= 0) return;
+        w.b = b;
+        w.load_seq();
+        w.unit = off >> 32 ? (int)(off / w.nb) : (int)((unsigned)off / (unsigned)w.nb);
+        w.blk_off = (int)(off - (long long)w.unit * w.nb);
+        part();
     }
-    __device__ bool done() const { return w.done(); }
+    __device__ bool done() const { return rest <= 0; }
     __device__ int tiles() const { return (len + 1) / 2; }
+    __device__ bool whole() const { return len == w.nb; }
     __device__ void next() {
-        w.advance(len);
-        len = w.done() ? 0 : w.seg_len();
+        rest -= len;
+        w.blk_off += len;
+        if (rest <= 0) return;
+        if (w.blk_off == w.nb) {
+            w.blk_off = 0;
+            if (++w.unit == w.units) {
+                w.unit = 0;
+                do { ++w.b; w.load_seq(); } while (w.nb == 0 && w.b + 1 < w.B);
+            }
+        }
+        part();
     }
 };
+
+// Where a CTA's range begins: blocks in it, sequence, blocks of that sequence
+// before it, and the length of the whole list.
+struct FbPlace {
+    int blocks, b;
+    long long off, W;
+};
+
+// plan_locate for at most 32 sequences and a list that 32 bits count, by each
+// warp for itself: one load, one scan, no barrier.
+template <bool G>
+__device__ __forceinline__ FbPlace fb_place(const PlanArgs &a, int cta, int lane,
+                                            unsigned *err) {
+    unsigned work = 0;
+    bool bad = false;
+    if (lane < a.B) {
+        int fb, sb;
+        work = (unsigned)visible_blocks<G>(a.seq_lens[lane], a.vis, a.max_blocks, &fb, &sb, &bad,
+                                           lane) *
+               a.units_per_seq;
+    }
+    unsigned x = work;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    const unsigned W = __shfl_sync(0xffffffffu, x, 31);
+    const unsigned P = min(W, (unsigned)a.num_ctas);
+    if (err && __any_sync(0xffffffffu, bad) && lane == 0) raise_error(err, kErrBadSeqLen);
+    FbPlace at{0, 0, 0, (long long)W};
+    if ((unsigned)cta >= P) return at;
+    const unsigned lo = (unsigned)cta * W / P, hi = ((unsigned)cta + 1u) * W / P;
+    const unsigned hit = __ballot_sync(0xffffffffu, x - work <= lo && lo < x);
+    at.b = __ffs(hit) - 1;
+    at.blocks = (int)(hi - lo);
+    at.off = lo - __shfl_sync(0xffffffffu, x - work, at.b);
+    return at;
+}
 
 struct FbUnit {      // what a unit's index stands for
     int kvh, row0, rows;
@@ -313,38 +407,31 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
     volatile int *abort_flag = &sh->abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (tid == 0) {
-        for (int s = 0; s < C::kKStages; ++s) {
-            mbar_init(&sh->k_full[s], 1);
-            mbar_init(&sh->k_empty[s], 1);
+    if (warp == 0) {
+        // the barriers, one lane each: arrivals that complete a phase
+        for (int i = lane; i < FbShared<NQ>::kBars; i += 32) {
+            uint64_t *bar = sh->k_full + i;
+            const uint32_t count = bar == &sh->mma_final ? 2             // both issuers
+                                   : bar >= sh->s_free ? 4               // warps
+                                   : bar >= sh->q_empty ? 9    // the issuer, the softmax warps
+                                                        : 1;
+            mbar_init(bar, count);
         }
-        for (int s = 0; s < C::kVStages; ++s) {
-            mbar_init(&sh->v_full[s], 1);
-            mbar_init(&sh->v_empty[s], 1);
+        if (lane == 0) {
+            sh->abort = 0;
+            tma_prefetch_map(&tm_k);
+            tma_prefetch_map(&tm_v);
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&sh->q_full[s], 1);
-            mbar_init(&sh->q_empty[s], 5);      // the S products' commit, four softmax warps
-            mbar_init(&sh->s_full[s], 1);
-            mbar_init(&sh->s_free[s], 4);
-            mbar_init(&sh->p_full[s], 4);
-            mbar_init(&sh->o_full[s], 1);
-            mbar_init(&sh->o_free[s], 4);
-        }
-        mbar_init(&sh->mma_final, 2);
-        sh->abort = 0;
         fence_barrier_init();
-        tma_prefetch_map(&tm_k);
-        tma_prefetch_map(&tm_v);
     }
     if (warp == 1) tmem_alloc(&sh->tmem_base, C::kTmemCols);
     // Rows of Q behind a unit's stay what they are: zeros from here on, or an
     // earlier unit's rows (their columns are never written out).
     for (int i = tid; i < 2 * C::kQBytes / 16; i += kFbThreads)
         reinterpret_cast<uint4 *>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = tid; i < 2 * NQ; i += kFbThreads) {
-        sh->qsc[i / NQ][i % NQ] = 0.f;
-        sh->row_i[i / NQ][i % NQ] = 0;
+    if (tid < 2 * NQ) {
+        sh->qsc[tid / NQ][tid % NQ] = 0.f;
+        sh->row_i[tid / NQ][tid % NQ] = 0;
     }
 
     // What came before on the stream wrote the inputs.
@@ -355,61 +442,80 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
     Visibility vis = p.vis;
     if (vis.window > 0) vis.window += p.q_len - 1;
     const int units = p.H_kv * p.chunks;
-    PlanArgs pa{p.seq_lens, p.B, units, vis, p.max_blocks, p.num_ctas};
-    plan_locate(pa, blockIdx.x, &sh->plan, nullptr, p.err);
+    const PlanArgs pa{p.seq_lens, p.B, units, vis, p.max_blocks, p.num_ctas};
+    FbWalk<G> walk;
+    long long W = 0;
+    if (p.whole_units) {
+        // one CTA per unit
+        const int b = blockIdx.x / units;
+        int fb, sb;
+        bool bad;
+        const int nb = visible_blocks<G>(p.seq_lens[b], vis, p.max_blocks, &fb, &sb, &bad, b);
+        if (bad && tid == 0) raise_error(p.err, kErrBadSeqLen);
+        walk.init(pa, nb, b, (long long)(blockIdx.x % units) * nb);
+    } else if (p.small_plan) {
+        const FbPlace at = fb_place<G>(pa, blockIdx.x, lane,
+                                       blockIdx.x == 0 && warp == 0 ? p.err : nullptr);
+        W = at.W;
+        walk.init(pa, at.blocks, at.b, at.off);
+    } else {
+        plan_locate(pa, blockIdx.x, &sh->plan, nullptr, p.err);
+        W = sh->plan.total;
+        const int P = working_ctas(W, p.num_ctas);
+        const bool works = (int)blockIdx.x < P;
+        const long long lo = works ? cta_bound(blockIdx.x, W, P) : 0;
+        const long long hi = works ? cta_bound(blockIdx.x + 1, W, P) : 0;
+        walk.init(pa, (int)(hi - lo), sh->plan.seq, lo - sh->plan.base);
+    }
+    // Table entries and scales of 32 blocks of the unit's part at a time, one
+    // per lane of warp 0; the first ones while the CTA is still setting up.
+    int my_row = 0;
+    float my_ks = 0.f, my_vs = 0.f;
+    bool my_block = false;
+    auto fetch = [&](int base) {
+        my_row = p.num_blocks * p.H_kv * kBlockSize;           // behind the pool: zeros
+        my_block = false;
+        if (base + lane < walk.len) {
+            const int phys = p.block_table[(size_t)walk.w.b * p.max_blocks +
+                                           walk.w.slot(walk.w.blk_off + base + lane)];
+            if (phys >= 0 && phys < p.num_blocks) {
+                const size_t at = (size_t)phys * p.H_kv + walk.w.unit / p.chunks;
+                my_row = (int)at * kBlockSize;
+                my_ks = p.k_scale[at];
+                my_vs = p.v_scale[at];
+                my_block = true;
+            } else {
+                raise_error(p.err, kErrBadBlock);
+            }
+        }
+    };
+    if (warp == 0 && !walk.done()) fetch(0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
-    const long long W = sh->plan.total;
-    const int P = working_ctas(W, p.num_ctas);
-    const bool works = (int)blockIdx.x < P;
-    const long long lo = works ? cta_bound(blockIdx.x, W, P) : 0;
-    const long long hi = works ? cta_bound(blockIdx.x + 1, W, P) : 0;
-    FbWalk<G> walk;
-    walk.init(pa, lo, hi, sh->plan.seq, sh->plan.base);
 
-    // Sequences without a visible key: rows of zeros.
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        int fb, sb;
-        bool bad;
-        if (visible_blocks<G>(p.seq_lens[b], vis, p.max_blocks, &fb, &sb, &bad, b) == 0) {
-            const size_t n = (size_t)p.q_len * p.H_q * D / 8;
-            uint4 *dst = reinterpret_cast<uint4 *>(p.out + (size_t)b * p.q_len * p.H_q * D);
-            for (size_t i = tid; i < n; i += kFbThreads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
+    if (warp >= 3) {
+        // The first unit's queries: all warps that have nothing else to do yet.
+        if (!walk.done())
+            fb_prepare_q<D, NQ>(p, walk.w.b, fb_unit(p, walk.w.unit), sQ, sh->qsc[0],
+                                sh->row_i[0], warp - 3, kFbThreads / 32 - 3);
+        fence_proxy_async_smem();
+        named_barrier(1, kFbThreads - 96);
     }
-
+    if (warp < 4) {
+    if constexpr (C::kSplitRegs) regs_decrease<C::kRegsLoad>();
     if (warp == 0) {
         // ============================================================ loads
         const uint64_t pol = l2_policy_evict_first();
         int tile = 0, n_k = 0, n_v = 0;         // tiles; copies of K and V issued (lane 0)
         bool ok = true;
-        for (; ok && !walk.done(); walk.next()) {
-            const FbUnit u = fb_unit(p, walk.w.unit);
-            // Table entries and scales of 32 blocks at a time, one per lane.
-            for (int base = 0; ok && base < walk.len; base += 32) {
-                int row = p.num_blocks * p.H_kv * kBlockSize;       // behind the pool: zeros
-                float4 info = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (base + lane < walk.len) {
-                    const int phys = p.block_table[(size_t)walk.w.b * p.max_blocks +
-                                                   walk.w.slot(walk.w.blk_off + base + lane)];
-                    if (phys >= 0 && phys < p.num_blocks) {
-                        const size_t at = (size_t)phys * p.H_kv + u.kvh;
-                        row = (int)at * kBlockSize;
-                        const float vs = p.v_scale[at];
-                        // A scale of 0 makes the values 0, not the weights: they
-                        // enter the sum through any other scale.
-                        const float vse = vs == 0.f ? 5.421010862427522e-20f /* 2^-64 */ : vs;
-                        info = make_float4(p.k_scale[at] * p.scale_log2, log2f(vse), 1.f / vse,
-                                           vs == 0.f ? 0.f : 1.f);
-                    } else {
-                        raise_error(p.err, kErrBadBlock);
-                    }
-                }
+        for (bool first = true; ok && !walk.done(); walk.next()) {
+            for (int base = 0; ok && base < walk.len; base += 32, first = false) {
+                if (!first) fetch(base);
                 for (int j = 0; ok && j < 32 && base + j < walk.len; j += 2, ++tile) {
-                    const int row0 = __shfl_sync(0xffffffffu, row, j);
-                    const int row1 = __shfl_sync(0xffffffffu, row, j + 1);
+                    const int row0 = __shfl_sync(0xffffffffu, my_row, j);
+                    const int row1 = __shfl_sync(0xffffffffu, my_row, j + 1);
                     const bool two = base + j + 1 < walk.len;
                     const uint32_t bytes = (two ? 2 : 1) * kBlockSize * D;
                     const int ks = tile % C::kKStages, vs = tile % C::kVStages;
@@ -437,7 +543,16 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) break;
-                    if (lane == j || lane == j + 1) sh->info[vs][lane - j] = info;
+                    if (lane == j || lane == j + 1) {
+                        // A scale of 0 makes the values 0, not the weights: they
+                        // enter the sum through any other scale.
+                        const float vse = my_vs == 0.f ? 5.421010862427522e-20f /* 2^-64 */
+                                                       : my_vs;
+                        sh->info[vs][lane - j] =
+                            my_block ? make_float4(my_ks * p.scale_log2, log2f(vse), 1.f / vse,
+                                                   my_vs == 0.f ? 0.f : 1.f)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&sh->v_full[vs], bytes);
@@ -470,32 +585,36 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             constexpr uint32_t idesc = fb_idesc(128, C::kN, 0, 0);
             constexpr int kLayout = C::kRowBytes == 128 ? 2 : 4;
             constexpr int kSteps = C::kRowBytes / 32;
-            int n = 0, seg = 0;
+            const uint64_t dk = fb_desc(smem_u32(sK), 16, C::kRowBytes * 8, kLayout);
+            const uint64_t dq = fb_desc(smem_u32(sQ), 16, C::kRowBytes * 8, kLayout);
+            int n = 0, seg = 0, ks = 0, turn = 0;          // slot of the ring, its round
             bool ok = true;
             for (; ok && !walk.done(); walk.next(), ++seg) {
-                ok = mbar_wait(&sh->q_full[seg & 1], (uint32_t)((seg >> 1) & 1), p.timeout_ns,
+                ok = mbar_poll(&sh->q_full[seg & 1], (uint32_t)((seg >> 1) & 1), p.timeout_ns,
                                p.err, abort_flag);
-                const uint32_t qb = smem_u32(sQ) + (seg & 1) * C::kQBytes;
                 for (int t = walk.tiles(); ok && t > 0; --t, ++n) {
-                    const int ks = n % C::kKStages;
-                    ok = mbar_wait(&sh->k_full[ks], (uint32_t)((n / C::kKStages) & 1),
-                                   p.timeout_ns, p.err, abort_flag) &&
-                         (n < 2 || mbar_wait(&sh->s_free[n & 1], (uint32_t)((n / 2 - 1) & 1),
-                                             p.timeout_ns, p.err, abort_flag));
+                    ok = (n < 2 || mbar_poll(&sh->s_free[n & 1], (uint32_t)((n / 2 - 1) & 1),
+                                             p.timeout_ns, p.err, abort_flag)) &&
+                         mbar_poll(&sh->k_full[ks], (uint32_t)(turn & 1), p.timeout_ns, p.err,
+                                   abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t kb = smem_u32(sK) + ks * C::kSlot;
 #pragma unroll
                     for (int s = 0; s < C::kBoxes * kSteps; ++s) {
                         const int x = s / kSteps, o = (s % kSteps) * 32;
+                        // addresses count in 16 bytes
                         umma_f8(tmem + C::kTmemS + (n & 1) * C::kN,
-                                fb_desc(kb + x * C::kBoxBytes + o, 16, C::kRowBytes * 8, kLayout),
-                                fb_desc(qb + x * C::kN * C::kRowBytes + o, 16, C::kRowBytes * 8,
-                                        kLayout),
+                                dk + ((ks * C::kSlot + x * C::kBoxBytes + o) >> 4),
+                                dq + (((seg & 1) * C::kQBytes + x * C::kN * C::kRowBytes + o) >>
+                                      4),
                                 idesc, s != 0);
                     }
                     umma_commit(&sh->s_full[n & 1]);
                     umma_commit(&sh->k_empty[ks]);
+                    if (++ks == C::kKStages) {
+                        ks = 0;
+                        ++turn;
+                    }
                 }
                 if (ok) umma_commit(&sh->q_empty[seg & 1]);
             }
@@ -507,31 +626,34 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (lane == 0) {
             constexpr uint32_t idesc = fb_idesc(C::kM, C::kN, 1, 1);
             constexpr int kLayout = C::kRowBytes == 128 ? 2 : 4;
-            int n = 0;
+            const uint64_t dv = fb_desc(smem_u32(sV), 16, C::kRowBytes * 8, kLayout);
+            const uint64_t dp = fb_desc(smem_u32(sP), 128, 2048, 0);
+            int n = 0, vs = 0, turn = 0;
             bool ok = true;
             for (; ok && !walk.done(); walk.next()) {
                 for (int t = walk.tiles(); ok && t > 0; --t, ++n) {
-                    const int vs = n % C::kVStages;
-                    ok = mbar_wait(&sh->v_full[vs], (uint32_t)((n / C::kVStages) & 1),
-                                   p.timeout_ns, p.err, abort_flag) &&
-                         (n < 2 || mbar_wait(&sh->o_free[n & 1], (uint32_t)((n / 2 - 1) & 1),
+                    ok = mbar_poll(&sh->v_full[vs], (uint32_t)(turn & 1), p.timeout_ns, p.err,
+                                   abort_flag) &&
+                         (n < 2 || mbar_poll(&sh->o_free[n & 1], (uint32_t)((n / 2 - 1) & 1),
                                              p.timeout_ns, p.err, abort_flag)) &&
-                         mbar_wait(&sh->p_full[n & 1], (uint32_t)((n >> 1) & 1), p.timeout_ns,
+                         mbar_poll(&sh->p_full[n & 1], (uint32_t)((n >> 1) & 1), p.timeout_ns,
                                    p.err, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t vb = smem_u32(sV) + vs * C::kSlot;
-                    const uint32_t pb = smem_u32(sP) + (n & 1) * C::kPBytes;
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
                         for (int s = 0; s < kFbTile / 32; ++s)
                             umma_f8(tmem + C::kTmemO + ((n & 1) * C::kHalves + h) * C::kN,
-                                    fb_desc(vb + h * C::kBoxBytes + s * 32 * C::kRowBytes, 16,
-                                            C::kRowBytes * 8, kLayout),
-                                    fb_desc(pb + s * 512, 128, 2048, 0), idesc, s != 0);
+                                    dv + ((vs * C::kSlot + h * C::kBoxBytes +
+                                           s * 32 * C::kRowBytes) >> 4),
+                                    dp + (((n & 1) * C::kPBytes + s * 512) >> 4), idesc, s != 0);
                     umma_commit(&sh->o_full[n & 1]);
                     umma_commit(&sh->v_empty[vs]);
+                    if (++vs == C::kVStages) {
+                        vs = 0;
+                        ++turn;
+                    }
                 }
             }
             umma_commit(&sh->mma_final);
@@ -540,15 +662,10 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         __syncwarp();
     } else {
-        // The first unit's queries: all warps that have nothing else to do yet.
-        if (!walk.done())
-            fb_prepare_q<D, NQ>(p, walk.w.b, fb_unit(p, walk.w.unit), sQ, sh->qsc[0],
-                                sh->row_i[0], warp - 3, kFbThreads / 32 - 3);
-        fence_proxy_async_smem();
-        named_barrier(1, kFbThreads - 96);
-        if (warp == 3) {
             // ================================================== next queries
-            for (int seg = 0; !walk.done(); ++seg) {
+            int seg = 0;
+            bool cut = false;          // the range's last unit goes on in the next CTA
+            for (; !walk.done(); ++seg) {
                 const int buf = seg & 1;
                 if (seg > 0) {
                     const bool ok =
@@ -561,51 +678,72 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                     fence_proxy_async_smem();
                 }
                 mbar_arrive_warp(&sh->q_full[buf]);
+                cut = walk.w.blk_off + walk.len < walk.w.nb;
                 walk.next();
             }
-        } else if (warp < 8) {
+            // What the second kernel has to join at this CTA's end: the CTAs
+            // that hold the unit, the first one's slot, sequence and unit.
+            if (!p.whole_units && lane == 0 && (int)blockIdx.x + 1 < p.num_ctas) {
+                FbCut c{0, -1, 0, 0, 0};
+                if (cut) {
+                    const int P = working_ctas(W, p.num_ctas);
+                    const long long su = cta_bound(blockIdx.x + 1, W, P) - walk.w.blk_off;
+                    c.first = cta_of(su, W, P);
+                    c.last = cta_of(su + walk.w.nb - 1, W, P);
+                    c.slot = 2 * c.first + (cta_bound(c.first, W, P) == su ? 0 : 1);
+                    c.b = walk.w.b;
+                    c.unit = walk.w.unit;
+                }
+                p.ws_cut[blockIdx.x] = c;
+            }
+    }
+    } else if (warp < 12) {
+            if constexpr (C::kSplitRegs) regs_increase<C::kRegsSoftmax>();
             // ======================================================= softmax
-            const int w = warp - 4, half = w >> 1;
+            const int grp = (warp - 4) >> 2, w = warp & 3, half = w >> 1;
             const int key = 32 * w + lane;                     // of the tile
             const uint32_t tlane = (uint32_t)(32 * w) << 16;
             const int L = p.q_len;
-            int n = 0, seg = 0;
+            float2 *ref = sh->ref[warp - 4];
+            float *grow = sh->grow[warp - 4];
+            int n = 0, seg = 0;                                // n: tiles before this unit's part
             bool ok = true;
             // Where a wait gives up, the warp goes on without waiting: the four
             // warps meet in a barrier at every tile, and none may miss it.
             auto wait = [&](uint64_t *bar, int phase) {
-                if (ok)
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(bar, (uint32_t)(phase & 1), p.timeout_ns, p.err,
-                                              abort_flag));
+                if (ok && !mbar_test(bar, (uint32_t)(phase & 1)))
+                    ok = mbar_wait(bar, (uint32_t)(phase & 1), p.timeout_ns, p.err, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
             };
-            for (; !walk.done(); walk.next(), ++seg) {
-                const int b = walk.w.b, T = walk.w.T;
-                const bool global = G && global_query(p.vis, b, T);
+            for (; !walk.done(); n += walk.tiles(), walk.next(), ++seg) {
+                const int T = walk.w.T, tiles = walk.tiles();
+                const bool global = G && global_query(p.vis, walk.w.b, T);
                 const int window = global ? 0 : p.vis.window, sink = p.vis.sink;
-                float l[NQ], top = -INFINITY;                  // top: of row lane
+                float2 l[NQ / 2];
+                float top = -INFINITY;                         // of row `lane`
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) l[q] = 0.f;
+                for (int q = 0; q < NQ / 2; ++q) l[q] = make_float2(0.f, 0.f);
                 wait(&sh->q_full[seg & 1], seg >> 1);
                 const float *qsc = sh->qsc[seg & 1];
-                const int tiles = walk.tiles();
-                for (int t = 0; t < tiles; ++t, ++n) {
-                    const int vs = n % C::kVStages, buf = n & 1;
+                for (int t = (n & 1) ^ grp; t < tiles; t += 2) {
+                    const int at_tile = n + t, round = at_tile >> 1;
+                    const int vs = at_tile % C::kVStages;
                     const bool there = 2 * t + half < walk.len;     // this warp's block
                     const int blk = walk.w.logical(walk.w.blk_off + 2 * t + (there ? half : 0));
                     const int first = blk * kBlockSize + 32 * (w & 1), pos = first + lane;
                     unsigned long long gmask = 0ull;
                     if (G && window > 0 && first <= T - 1 - window)
-                        gmask = global_mask(p.vis, b, blk, lane);
+                        gmask = global_mask(p.vis, walk.w.b, blk, lane);
                     // every key of the warp seen by every query
                     const bool all = there && first + 31 <= T - L &&
                                      (window <= 0 || first > T - 1 - window || first + 31 < sink);
-                    wait(&sh->v_full[vs], n / C::kVStages);
+                    wait(&sh->v_full[vs], at_tile / C::kVStages);
                     const float4 info = sh->info[vs][half];
-                    if (!all) {
+                    if (!all || info.w == 0.f) {
                         // Rows that no query sees may hold NaN codes: they are
-                        // zeroed, since 0 x NaN would reach every row's sum.
-                        const bool any = there && pos < T &&
+                        // zeroed, since 0 x NaN would reach every row's sum.  So
+                        // are those whose scale is 0.
+                        const bool any = there && pos < T && info.w != 0.f &&
                                          (window <= 0 || pos > T - L - window || pos < sink ||
                                           ((gmask >> (pos & 63)) & 1ull));
                         if (!any) {
@@ -618,34 +756,54 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                                         make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
-                    wait(&sh->s_full[buf], n >> 1);
+                    wait(&sh->s_full[grp], round);
                     tc_fence_after();
-                    float s[C::kN];
-                    fb_tmem_ld<C::kN>(tmem + C::kTmemS + buf * C::kN + tlane, s);
-                    tc_fence_before();
-                    mbar_arrive_warp(&sh->s_free[buf]);
-
-                    // scores in log2 units, the V scale's exponent among them
+                    float2 s[NQ / 2];
+                    {
+                        float x[NQ], y[NQ];
+                        const uint32_t at = tmem + C::kTmemS + grp * C::kN + tlane;
+                        if constexpr (NQ == 8) {
+                            float xy[16];
+                            tmem_ld16(at, xy);
 #pragma unroll
-                    for (int q = 0; q < NQ; q += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(qsc + q);
-                        s[q] = fmaf(fmaf(s[NQ + q], 0.03125f, s[q]), f.x * info.x, info.y);
-                        s[q + 1] =
-                            fmaf(fmaf(s[NQ + q + 1], 0.03125f, s[q + 1]), f.y * info.x, info.y);
-                        s[q + 2] =
-                            fmaf(fmaf(s[NQ + q + 2], 0.03125f, s[q + 2]), f.z * info.x, info.y);
-                        s[q + 3] =
-                            fmaf(fmaf(s[NQ + q + 3], 0.03125f, s[q + 3]), f.w * info.x, info.y);
+                            for (int q = 0; q < 8; ++q) {
+                                x[q] = xy[q];
+                                y[q] = xy[8 + q];
+                            }
+                        } else {
+                            fb_tmem_ld<NQ>(at, x);
+                            fb_tmem_ld<NQ>(at + NQ, y);
+                        }
+                        tc_fence_before();
+                        mbar_arrive_warp(&sh->s_free[grp]);
+                        // scores in log2 units, the V scale's exponent among them
+                        const float2 k2 = make_float2(info.x, info.x);
+                        const float2 v2 = make_float2(info.y, info.y);
+                        const float2 part = make_float2(0.03125f, 0.03125f);
+#pragma unroll
+                        for (int q = 0; q < NQ; q += 4) {
+                            const float4 f = *reinterpret_cast<const float4 *>(qsc + q);
+                            s[q / 2] = __ffma2_rn(
+                                __ffma2_rn(make_float2(y[q], y[q + 1]), part,
+                                           make_float2(x[q], x[q + 1])),
+                                __fmul2_rn(make_float2(f.x, f.y), k2), v2);
+                            s[q / 2 + 1] = __ffma2_rn(
+                                __ffma2_rn(make_float2(y[q + 2], y[q + 3]), part,
+                                           make_float2(x[q + 2], x[q + 3])),
+                                __fmul2_rn(make_float2(f.z, f.w), k2), v2);
+                        }
                     }
                     if (!all) {
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
+                        auto seen = [&](int q) {
                             const int at = T - L + (L > 1 ? sh->row_i[seg & 1][q] : 0);
-                            const bool seen =
-                                there && pos <= at &&
-                                (window <= 0 || pos > at - window || pos < sink ||
-                                 ((gmask >> (pos & 63)) & 1ull));
-                            if (!seen) s[q] = -INFINITY;
+                            return there && pos <= at &&
+                                   (window <= 0 || pos > at - window || pos < sink ||
+                                    ((gmask >> (pos & 63)) & 1ull));
+                        };
+#pragma unroll
+                        for (int q = 0; q < NQ; q += 2) {
+                            if (!seen(q)) s[q / 2].x = -INFINITY;
+                            if (!seen(q + 1)) s[q / 2].y = -INFINITY;
                         }
                     }
                     // largest of the tile, per row
@@ -653,217 +811,322 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                         float mine = 0.f;
 #pragma unroll
                         for (int q = 0; q < NQ; ++q) {
-                            const float m = warp_max(s[q]);
+                            const float m = warp_max(q & 1 ? s[q / 2].y : s[q / 2].x);
                             if (lane == q) mine = m;
                         }
-                        if (lane < NQ) sh->wmax[buf][w][lane] = mine;
+                        // The P buffer and what goes with it are free again: the
+                        // group's last tile is through, wmax read by all.
+                        if (round >= 1) wait(&sh->o_free[grp], round - 1);
+                        if (lane < NQ) sh->wmax[grp][w][lane] = mine;
                     }
-                    // the P buffer and what goes with it are free again
-                    if (n >= 2) wait(&sh->o_free[buf], n / 2 - 1);
-                    named_barrier(2, 128);
+                    named_barrier(2 + grp, 128);
                     bool grew = false;
                     if (lane < NQ) {
-                        const float m = fmaxf(fmaxf(sh->wmax[buf][0][lane], sh->wmax[buf][1][lane]),
-                                              fmaxf(sh->wmax[buf][2][lane],
-                                                    sh->wmax[buf][3][lane]));
+                        const float m = fmaxf(fmaxf(sh->wmax[grp][0][lane], sh->wmax[grp][1][lane]),
+                                              fmaxf(sh->wmax[grp][2][lane],
+                                                    sh->wmax[grp][3][lane]));
                         const float now = m != m ? m : fmaxf(top, m);
-                        // factor of this tile (2^8 in its weights), of what came before
-                        const float c = m == -INFINITY ? 0.f : exp2f(m - now - 8.f);
-                        const float a = top == now ? 1.f : exp2f(top - now);
-                        sh->ref[w][lane] = make_float2(m == -INFINITY ? 0.f : m - 8.f, c);
-                        sh->grow[w][lane] = a;
+                        // factor of this tile's weights (2^8 in them) in the sum
+                        const float c = m == -INFINITY ? 0.f : exp2_approx(m - now - 8.f);
+                        const float a = top == now ? 1.f : exp2_approx(top - now);
+                        ref[lane] = make_float2(m == -INFINITY ? 0.f : 8.f - m, c * info.z);
+                        grow[lane] = a;
                         grew = a != 1.f;
                         top = now;
-                        if (w == 0) sh->join[buf][lane] = make_float2(c, a);
+                        if (w == 0) sh->top[grp][lane] = m;
                     }
                     grew = __any_sync(0xffffffffu, grew);
                     __syncwarp();
                     if (grew) {
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q) l[q] *= sh->grow[w][q];
+                        for (int q = 0; q < NQ; q += 2)
+                            l[q / 2] = __fmul2_rn(l[q / 2],
+                                                  *reinterpret_cast<const float2 *>(grow + q));
                     }
-                    uint32_t hi[NQ / 4], lo_[NQ / 4];
+                    uint32_t hi[NQ / 4], lo[NQ / 4];
 #pragma unroll
                     for (int q = 0; q < NQ; q += 2) {
-                        const float4 r = *reinterpret_cast<const float4 *>(&sh->ref[w][q]);
-                        const float a = exp2_approx(s[q] - r.x), c = exp2_approx(s[q + 1] - r.z);
-                        l[q] = fmaf(a, r.y * info.z, l[q]);
-                        l[q + 1] = fmaf(c, r.w * info.z, l[q + 1]);
+                        const float4 r = *reinterpret_cast<const float4 *>(&ref[q]);
+                        float2 x = __fadd2_rn(s[q / 2], make_float2(r.x, r.z));
+                        x.x = exp2_approx(x.x);
+                        x.y = exp2_approx(x.y);
+                        l[q / 2] = __ffma2_rn(x, make_float2(r.y, r.w), l[q / 2]);
                         uint32_t h2, l2;
-                        e4m3_split2(a * info.w, c * info.w, h2, l2);
+                        e4m3_split2(x.x, x.y, h2, l2);
                         if (q % 4 == 0) {
                             hi[q / 4] = h2;
-                            lo_[q / 4] = l2;
+                            lo[q / 4] = l2;
                         } else {
                             hi[q / 4] |= h2 << 16;
-                            lo_[q / 4] |= l2 << 16;
+                            lo[q / 4] |= l2 << 16;
                         }
                     }
                     // 16 columns of a key are 16 bytes, keys one after another
-                    unsigned char *pk = sP + buf * C::kPBytes + key * 16;
+                    unsigned char *pk = sP + grp * C::kPBytes + key * 16;
                     if constexpr (NQ == 8) {
-                        *reinterpret_cast<uint4 *>(pk) = make_uint4(hi[0], hi[1], lo_[0], lo_[1]);
+                        *reinterpret_cast<uint4 *>(pk) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
                     } else {
 #pragma unroll
                         for (int g = 0; g < NQ / 16; ++g) {
                             *reinterpret_cast<uint4 *>(pk + g * 2048) = make_uint4(
                                 hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
                             *reinterpret_cast<uint4 *>(pk + (NQ / 16 + g) * 2048) = make_uint4(
-                                lo_[4 * g], lo_[4 * g + 1], lo_[4 * g + 2], lo_[4 * g + 3]);
+                                lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
                         }
                     }
-                    if (t == tiles - 1) {
-                        const float sum = warp_sums<NQ>(l, lane);
+                    if (t + 2 >= tiles) {              // the group's last of the unit
+                        float v[NQ];
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) v[q] = q & 1 ? l[q / 2].y : l[q / 2].x;
+                        const float sum = warp_sums<NQ>(v, lane);
                         if (lane < NQ) {
-                            sh->lsum[buf][w][lane] = sum;
-                            if (w == 0) sh->top[buf][lane] = top;
+                            sh->lsum[seg & 1][grp][w][lane] = sum;
+                            if (w == 0) sh->ltop[seg & 1][grp][lane] = top;
                         }
-                        mbar_arrive_warp(&sh->q_empty[seg & 1]);
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive_warp(&sh->p_full[buf]);
+                    mbar_arrive_warp(&sh->p_full[grp]);
                 }
+                mbar_arrive_warp(&sh->q_empty[seg & 1]);
             }
-        } else {
+    } else {
+            if constexpr (C::kSplitRegs) regs_increase<C::kRegsOutput>();
             // ======================================================== output
             const int w = warp & 3;
             const uint32_t tlane = (uint32_t)(32 * w) << 16;
             const int col = C::kM == 64 ? 16 * w + lane : 32 * w + lane;
             const bool mine = C::kM == 128 || lane < 16;
-            int n = 0;
-            bool ok = true, first_seg = true;
+            float2 *join = sh->join[w];
+            int n = 0, seg = 0;
+            bool ok = true;
             auto wait = [&](uint64_t *bar, int phase) {
-                return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1), p.timeout_ns,
-                                                         p.err, abort_flag));
+                if (ok && !mbar_test(bar, (uint32_t)(phase & 1)))
+                    ok = mbar_wait(bar, (uint32_t)(phase & 1), p.timeout_ns, p.err, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
             };
-            for (; ok && !walk.done(); walk.next(), first_seg = false) {
-                float o[C::kHalves][NQ];
+            for (; ok && !walk.done(); walk.next(), ++seg) {
+                float2 o[C::kHalves][NQ / 2];
+                float top = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) o[h][q] = 0.f;
-                const int tiles = walk.tiles();
+                    for (int q = 0; q < NQ / 2; ++q) o[h][q] = make_float2(0.f, 0.f);
+                const int tiles = walk.tiles(), n0 = n;
                 for (int t = 0; ok && t < tiles; ++t, ++n) {
                     const int buf = n & 1;
-                    ok = wait(&sh->p_full[buf], n >> 1) && wait(&sh->o_full[buf], n >> 1);
+                    wait(&sh->p_full[buf], n >> 1);
+                    if (lane < NQ) {
+                        const float m = sh->top[buf][lane];
+                        const float now = m != m ? m : fmaxf(top, m);
+                        // a tile that the row does not see adds nothing
+                        join[lane] = make_float2(
+                            m == -INFINITY ? 0.f : exp2_approx(m - now - 8.f),
+                            top == now ? 1.f : exp2_approx(top - now));
+                        top = now;
+                    }
+                    __syncwarp();
+                    wait(&sh->o_full[buf], n >> 1);
                     if (!ok) break;
                     tc_fence_after();
+                    constexpr int kCols = NQ < 16 ? NQ : 16;
+                    const float2 part = make_float2(0.03125f, 0.03125f);
 #pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h) {
-                        float x[C::kN];
-                        fb_tmem_ld<C::kN>(
-                            tmem + C::kTmemO + (buf * C::kHalves + h) * C::kN + tlane, x);
+                    for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-                        for (int q = 0; q < NQ; q += 2) {
-                            const float4 f = *reinterpret_cast<const float4 *>(&sh->join[buf][q]);
-                            o[h][q] = fmaf(fmaf(x[NQ + q], 0.03125f, x[q]), f.x, o[h][q] * f.y);
-                            o[h][q + 1] = fmaf(fmaf(x[NQ + q + 1], 0.03125f, x[q + 1]), f.z,
-                                               o[h][q + 1] * f.w);
+                        for (int q0 = 0; q0 < NQ; q0 += kCols) {
+                            float xy[2 * kCols];
+                            const uint32_t at =
+                                tmem + C::kTmemO + (buf * C::kHalves + h) * C::kN + tlane;
+                            if constexpr (NQ <= 16) {
+                                fb_tmem_ld<2 * kCols>(at, xy);
+                            } else {
+                                tmem_ld16(at + q0, xy);
+                                tmem_ld16(at + NQ + q0, xy + 16);
+                            }
+#pragma unroll
+                            for (int q = 0; q < kCols; q += 2) {
+                                const float4 f =
+                                    *reinterpret_cast<const float4 *>(&join[q0 + q]);
+                                float2 &d = o[h][(q0 + q) / 2];
+                                const float2 v = __ffma2_rn(
+                                    make_float2(xy[kCols + q], xy[kCols + q + 1]), part,
+                                    make_float2(xy[q], xy[q + 1]));
+                                d = __ffma2_rn(v, make_float2(f.x, f.z),
+                                               __fmul2_rn(d, make_float2(f.y, f.w)));
+                            }
                         }
-                    }
                     if (t == tiles - 1) {
                         const FbUnit u = fb_unit(p, walk.w.unit);
-                        const bool whole = walk.w.blk_off == 0 && walk.len == walk.w.nb;
-                        const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
-                        float *part = p.ws_o + (size_t)slot * NQ * D;
+                        float sum = 0.f;               // of row `lane`
+                        int out_row = 0;
+                        if (lane < u.rows) {
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            if (q >= u.rows) break;
-                            const float sum = (sh->lsum[buf][0][q] + sh->lsum[buf][1][q]) +
-                                              (sh->lsum[buf][2][q] + sh->lsum[buf][3][q]);
-                            if (!whole) {
-#pragma unroll
-                                for (int h = 0; h < C::kHalves; ++h)
-                                    if (mine) part[q * D + h * 128 + col] = o[h][q];
-                                if (w == 0 && lane == 0)
-                                    p.ws_ml[slot * NQ + q] = make_float2(sh->top[buf][q], sum);
-                            } else {
-                                const int row = u.row0 + q, i = row / p.group, g = row % p.group;
-                                __nv_bfloat16 *dst =
-                                    p.out + ((size_t)(walk.w.b * p.q_len + i) * p.H_q +
-                                             u.kvh * p.group + g) * D;
-#pragma unroll
-                                for (int h = 0; h < C::kHalves; ++h)
-                                    if (mine)
-                                        dst[h * 128 + col] = __float2bfloat16_rn(
-                                            sum != 0.f ? o[h][q] / sum : 0.f);
+                            for (int g = 0; g < 2; ++g) {
+                                // the group has a tile of this part
+                                if (tiles < 2 && (n0 & 1) != g) continue;
+                                const float lt = sh->ltop[seg & 1][g][lane];
+                                const float *ls = &sh->lsum[seg & 1][g][0][lane];
+                                const float s = (ls[0] + ls[NQ]) + (ls[2 * NQ] + ls[3 * NQ]);
+                                if (lt != -INFINITY) sum = fmaf(s, exp2_approx(lt - top), sum);
                             }
+                            const int row = u.row0 + lane, i = row / p.group;
+                            out_row = (walk.w.b * p.q_len + i) * p.H_q + u.kvh * p.group +
+                                      (row - i * p.group);
+                        }
+                        if (walk.whole()) {
+                            const float by = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) {
+                                const float f = __shfl_sync(0xffffffffu, by, q);
+                                __nv_bfloat16 *dst =
+                                    p.out +
+                                    (size_t)__shfl_sync(0xffffffffu, out_row, q) * D + col;
+                                if (q < u.rows && mine) {
+#pragma unroll
+                                    for (int h = 0; h < C::kHalves; ++h)
+                                        dst[h * 128] = __float2bfloat16_rn(
+                                            (q & 1 ? o[h][q / 2].y : o[h][q / 2].x) * f);
+                                }
+                            }
+                        } else {
+                            const int slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
+                            float *part_o = p.ws_o + (size_t)slot * NQ * D + col;
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q)
+                                if (q < u.rows && mine) {
+#pragma unroll
+                                    for (int h = 0; h < C::kHalves; ++h)
+                                        part_o[q * D + h * 128] =
+                                            q & 1 ? o[h][q / 2].y : o[h][q / 2].x;
+                                }
+                            if (w == 0 && lane < u.rows)
+                                p.ws_ml[slot * NQ + lane] = make_float2(top, sum);
                         }
                     }
                     tc_fence_before();
                     mbar_arrive_warp(&sh->o_free[buf]);
                 }
             }
-        }
     }
 
+    // Sequences without a visible key: rows of zeros.
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        int fb, sb;
+        bool bad;
+        if (visible_blocks<G>(p.seq_lens[b], vis, p.max_blocks, &fb, &sb, &bad, b) == 0) {
+            const size_t n = (size_t)p.q_len * p.H_q * D / 8;
+            uint4 *dst = reinterpret_cast<uint4 *>(p.out + (size_t)b * p.q_len * p.H_q * D);
+            for (size_t i = tid; i < n; i += kFbThreads) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// Joins the partials of the unit that holds the boundary between main CTAs i
-// and i + 1 (i = blockIdx.x), if it lies inside one.  The CTAs of a unit's
-// boundaries share its values; splits are added in order, so a result does
-// not depend on which CTA came first.
+// Joins the partials of the unit that is cut between main CTAs i and i + 1
+// (i = blockIdx.x), if one is.  The CTAs of a unit's cuts share its values;
+// splits are added in order, so a result does not depend on which CTA came
+// first.
 constexpr int kFbJoinThreads = 256;
 template <int D, int NQ>
 __global__ void __launch_bounds__(kFbJoinThreads)
 gqa_fp8_block_join_kernel(const GqaFp8BlockParams p) {
-    __shared__ PlanScratch sc;
-    const int tid = threadIdx.x;
-    Visibility vis = p.vis;
-    if (vis.window > 0) vis.window += p.q_len - 1;
-    const int units = p.H_kv * p.chunks;
-    const PlanArgs pa{p.seq_lens, p.B, units, vis, p.max_blocks, p.num_ctas};
-    // the lengths were there before the main kernel began
-    plan_locate(pa, blockIdx.x + 1, &sc, nullptr, nullptr);
-    const long long W = sc.total;
-    const int P = working_ctas(W, p.num_ctas);
+    constexpr int kWarps = kFbJoinThreads / 32;
+    constexpr int kC = D / 4;                  // float4 of a row
+    constexpr int kPer = D == 256 ? 2 : 1;     // of a lane
+    constexpr int kPar = D == 64 ? 2 : 1;      // splits that a warp adds at a time
+    constexpr int kAhead = 4;
+    __shared__ float4 s_o[kWarps][kC * kPar];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_wait_primary();
-    if ((int)blockIdx.x + 1 >= P) return;
-    const long long x = cta_bound(blockIdx.x + 1, W, P);
-    int fb, sb;
-    bool bad;
-    const int b = sc.seq;
-    const int nb = visible_blocks(p.seq_lens[b], vis, p.max_blocks, &fb, &sb, &bad, b);
-    const int unit = (int)((x - sc.base) / nb);
-    const long long su = sc.base + (long long)unit * nb, eu = su + nb;
-    if (x == su) return;
-    const int c0 = cta_of(su, W, P), c1 = cta_of(eu - 1, W, P);
-    const int slot0 = 2 * c0 + (cta_bound(c0, W, P) == su ? 0 : 1);
-    const FbUnit u = fb_unit(p, unit);
-    // float4 items of the unit, dealt out over its boundaries' CTAs
-    const int items = u.rows * (D / 4), n = c1 - c0;
-    for (int it = ((int)blockIdx.x - c0) * kFbJoinThreads + tid; it < items;
-         it += n * kFbJoinThreads) {
-        const int q = it / (D / 4), c = (it % (D / 4)) * 4;
-        float top = -INFINITY;
-        for (int k = c0; k <= c1; ++k)
-            top = fmaxf(top, p.ws_ml[(k == c0 ? slot0 : 2 * k) * NQ + q].x);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll 4
-        for (int k = c0; k <= c1; ++k) {
-            const int slot = k == c0 ? slot0 : 2 * k;
-            const float2 ml = p.ws_ml[slot * NQ + q];
-            const float4 v =
-                *reinterpret_cast<const float4 *>(p.ws_o + ((size_t)slot * NQ + q) * D + c);
-            // a split whose keys the row does not see has top -inf and sum 0
-            const float a = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-            sum = fmaf(a, ml.y, sum);
-            o.x = fmaf(a, v.x, o.x);
-            o.y = fmaf(a, v.y, o.y);
-            o.z = fmaf(a, v.z, o.z);
-            o.w = fmaf(a, v.w, o.w);
+    const FbCut cut = p.ws_cut[blockIdx.x];
+    if (cut.last < cut.first) return;
+    const FbUnit u = fb_unit(p, cut.unit);
+    const int n = cut.last - cut.first + 1;    // splits
+    const int sub = kPar == 2 ? lane >> 4 : 0, c = kPar == 2 ? lane & 15 : lane;
+    auto slot = [&](int k) { return k == 0 ? cut.slot : 2 * (cut.first + k); };
+    for (int q = (int)blockIdx.x - cut.first; q < u.rows; q += n - 1) {
+        // Warp w adds splits w, w + 8, ... (two at once where a row is short),
+        // each lane its columns, relative to the largest reference of them.
+        float top = -INFINITY, sum = 0.f;
+        float4 o[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = warp * kPar + sub; k0 < n; k0 += kAhead * kWarps * kPar) {
+            float2 ml[kAhead];
+            float4 v[kAhead][kPer];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                const int k = k0 + a * kWarps * kPar;
+                ml[a] = make_float2(-INFINITY, 0.f);
+                if (k < n) {
+                    const size_t at = (size_t)slot(k) * NQ + q;
+                    ml[a] = p.ws_ml[at];
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j)
+                        v[a][j] = *reinterpret_cast<const float4 *>(p.ws_o + at * D +
+                                                                    (j * 32 + c) * 4);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                // a split whose keys the row does not see adds nothing
+                if (ml[a].x == -INFINITY) continue;
+                const float now = ml[a].x != ml[a].x ? ml[a].x : fmaxf(top, ml[a].x);
+                const float f = exp2f(ml[a].x - now);
+                const float g = top == now ? 1.f : exp2f(top - now);
+                top = now;
+                sum = fmaf(sum, g, ml[a].y * f);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    o[j].x = fmaf(o[j].x, g, v[a][j].x * f);
+                    o[j].y = fmaf(o[j].y, g, v[a][j].y * f);
+                    o[j].z = fmaf(o[j].z, g, v[a][j].z * f);
+                    o[j].w = fmaf(o[j].w, g, v[a][j].w * f);
+                }
+            }
         }
-        const float by = sum != 0.f ? 1.f / sum : 0.f;
-        const int row = u.row0 + q, i = row / p.group, g = row % p.group;
-        __nv_bfloat162 r[2] = {__floats2bfloat162_rn(o.x * by, o.y * by),
-                               __floats2bfloat162_rn(o.z * by, o.w * by)};
-        *reinterpret_cast<uint2 *>(p.out + ((size_t)(b * p.q_len + i) * p.H_q + u.kvh * p.group +
-                                            g) * D + c) = *reinterpret_cast<const uint2 *>(r);
+        // ... and the warps' sums, in order
+        __shared__ float s_top[kWarps * kPar];
+        __shared__ float s_part[kWarps * kPar];
+        __syncthreads();                       // the last row's are read
+        if (c == 0) {
+            s_top[warp * kPar + sub] = top;
+            s_part[warp * kPar + sub] = sum;
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) s_o[warp][(kPar == 2 ? sub * kC : j * 32) + c] = o[j];
+        __syncthreads();
+        if (tid < kC) {
+            float all = -INFINITY;
+            bool nan = false;
+#pragma unroll
+            for (int k = 0; k < kWarps * kPar; ++k) {
+                nan |= s_top[k] != s_top[k];
+                all = fmaxf(all, s_top[k]);
+            }
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+            float total = nan ? NAN : 0.f;
+#pragma unroll
+            for (int k = 0; k < kWarps * kPar; ++k) {
+                const float f = s_top[k] == -INFINITY ? 0.f : exp2f(s_top[k] - all);
+                const float4 x = s_o[k / kPar][(k % kPar) * kC + tid];
+                total = fmaf(f, s_part[k], total);
+                r.x = fmaf(f, x.x, r.x);
+                r.y = fmaf(f, x.y, r.y);
+                r.z = fmaf(f, x.z, r.z);
+                r.w = fmaf(f, x.w, r.w);
+            }
+            const float by = total != 0.f ? 1.f / total : 0.f;
+            const int row = u.row0 + q, i = row / p.group, g = row % p.group;
+            __nv_bfloat162 w[2] = {__floats2bfloat162_rn(r.x * by, r.y * by),
+                                   __floats2bfloat162_rn(r.z * by, r.w * by)};
+            *reinterpret_cast<uint2 *>(p.out + ((size_t)(cut.b * p.q_len + i) * p.H_q +
+                                                u.kvh * p.group + g) * D + tid * 4) =
+                *reinterpret_cast<const uint2 *>(w);
+        }
     }
 }
 
@@ -878,7 +1141,7 @@ static int fb_columns(int chunk_rows) { return chunk_rows <= 8 ? 8 : chunk_rows 
 
 int64_t fp8_block_workspace_bytes(int num_ctas, int rows, int d) {
     const int64_t nq = fb_columns(fp8_block_rows(rows));
-    return 2ll * num_ctas * nq * (d * 4 + 8) + 256;
+    return 2ll * num_ctas * nq * (d * 4 + 8) + num_ctas * (int64_t)sizeof(FbCut);
 }
 
 namespace {
@@ -904,6 +1167,12 @@ cudaError_t fb_launch(const GqaFp8BlockParams &p, cudaStream_t stream) {
     using C = FbCfg<D, NQ>;
     static PerDeviceFlag configured;
     cudaError_t e = configure_once_per_device(configured, [] {
+        // The shares of a register split must fit in what the kernel is
+        // launched with, or the increase would never be granted.
+        cudaFuncAttributes fa;
+        const cudaError_t r = cudaFuncGetAttributes(&fa, gqa_fp8_block_kernel<D, NQ, G>);
+        if (r != cudaSuccess) return r;
+        if (C::kSplitRegs && fa.numRegs < 128) return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(gqa_fp8_block_kernel<D, NQ, G>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
@@ -916,14 +1185,14 @@ cudaError_t fb_launch(const GqaFp8BlockParams &p, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.num_ctas);
+    cfg.gridDim = dim3((unsigned)(p.whole_units ? p.B * p.H_kv * p.chunks : p.num_ctas));
     cfg.blockDim = dim3(kFbThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, gqa_fp8_block_kernel<D, NQ, G>, tk, tv, p);
-    if (e != cudaSuccess || p.num_ctas == 1) return e;
+    if (e != cudaSuccess || p.whole_units || p.num_ctas == 1) return e;
     cfg.gridDim = dim3((unsigned)p.num_ctas - 1);
     cfg.blockDim = dim3(kFbJoinThreads);
     cfg.dynamicSmemBytes = 0;
@@ -951,6 +1220,13 @@ cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &given, int d, void *wo
     const size_t slots = 2 * (size_t)p.num_ctas * fb_columns(p.chunk_rows);
     p.ws_o = static_cast<float *>(workspace);
     p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + slots * d);
+    p.ws_cut = reinterpret_cast<FbCut *>(p.ws_ml + slots);
+    // Where no sequence can be long and there is an SM for every unit, a unit
+    // is not split: that saves the second kernel.
+    p.whole_units = p.max_blocks <= kFbWholeBlocks &&
+                    (long long)p.B * p.H_kv * p.chunks <= p.num_ctas;
+    p.small_plan = p.B <= 32 &&
+                   (double)p.B * p.H_kv * p.chunks * p.max_blocks * (p.num_ctas + 1.0) < 4e9;
     switch (d) {
         case 64: return fb_launch_d<64>(p, stream);
         case 128: return fb_launch_d<128>(p, stream);

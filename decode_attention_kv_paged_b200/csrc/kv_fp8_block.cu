@@ -1,20 +1,27 @@
 // kv_fp8_block.cu -- append to and read back the block-scaled fp8 cache.
 //
-// One CTA per (64-token block that a run touches, head, K or V): a block's
-// scale is the power of two that its largest new value asks for, so one CTA
-// sees every new row of the block, holds them in registers between finding
-// the maximum and writing the codes, and reads each input once.
+// Append: one CTA per (64-token block that a run touches, head, K or V).  A
+// block's scale is the power of two that its largest new value asks for, so
+// one CTA sees every new row of the block, holds them in registers between
+// finding the maximum and writing the codes, and reads each input once.
+// Read-back: one CTA per (block, up to 8 heads, K or V), 16-byte stores.
+// Both are bound by memory; what is left beside that is the chain of dependent
+// loads that finds a CTA its rows (offsets and positions, block table, data).
 #include <cuda_fp8.h>
 
 #include "fp8_block.cuh"
 
 namespace attn {
 
+constexpr int kRunThreads = 256;
+
 // Part of a run that falls into one block.
 struct BlockRun {
-    int src;        // input row of the block's first new row
+    int b;          // sequence
+    int src;        // row of the block's first new row among the call's rows
     int r0, r1;     // rows [r0, r1) of the block
-    int phys;       // physical block, -1: not there (flagged) or nothing to do
+    int slot;       // table slot, -1: not one of the sequence's blocks
+    bool replaced;  // a later block of the run takes the slot
 };
 
 // The part of a run that CTA column x of the grid works on.  Sequence b owns
@@ -22,14 +29,15 @@ struct BlockRun {
 // rows touches at most (n + 62) / 64 + 1 blocks, which is never more than the
 // floor(o' / 64) - floor(o / 64) + 2 columns between o and o' = o + n.  So the
 // columns need no prefix sum over block counts; 32 lanes probe the offsets at
-// once to find b (two rounds for up to 1024 sequences).  Every thread of the
+// once to find b (one round for up to 32 sequences, two for 1024), and the
+// last round brings the run's end and position along.  Every thread of the
 // CTA gets the same answer; false where the column has no work.  flag: this
-// thread reports what is wrong with the run.  reading: rows whose ring slot a
-// later block of the run holds are an error (a writer just leaves them out).
-__device__ __forceinline__ bool locate_run(const KvRunParams &p, int x, bool flag, bool reading,
+// thread reports what is wrong with the run.  rest: the rows behind the last
+// sequence are handed out as a run without blocks.
+__device__ __forceinline__ bool locate_run(const KvRunParams &p, int x, bool flag, bool rest,
                                            BlockRun *out) {
     const int lane = threadIdx.x & 31;
-    int b, o0, n, ord;
+    int b, o0, n, ord, pos;
     if (p.offsets) {
         // the first column reports offsets that are wrong: the search below may
         // not meet the sequence that has them
@@ -38,56 +46,75 @@ __device__ __forceinline__ bool locate_run(const KvRunParams &p, int x, bool fla
                 const int a = p.offsets[i], e = p.offsets[i + 1];
                 if (a < 0 || e < a || e > p.n_tokens) raise_error(p.err, kErrBadSeqLen);
             }
-        int lo = 0, hi = p.B;
-        while (hi - lo > 1) {
+        int lo = 0, hi = p.B + (rest ? 1 : 0), o1;
+        for (;;) {
             const int step = (hi - lo + 31) / 32;
             const int i = lo + lane * step;
-            const bool below = i < hi && (long long)p.offsets[i] / 64 + 2ll * i <= x;
-            const unsigned m = __ballot_sync(0xffffffffu, below);
+            const bool in = i < hi;
+            const int o = in ? p.offsets[i] : 0;
+            int end = 0, at = -1;
+            if (step == 1 && in) {
+                end = i < p.B ? p.offsets[i + 1] : p.n_tokens;
+                if (i < p.B) at = p.positions[i];
+            }
+            const unsigned m =
+                __ballot_sync(0xffffffffu, in && (long long)o / 64 + 2ll * i <= x);
             if (m == 0) return false;              // before the first row
-            lo += (31 - __clz(m)) * step;
+            const int sel = 31 - __clz(m);
+            if (step == 1) {
+                b = lo + sel;
+                o0 = __shfl_sync(0xffffffffu, o, sel);
+                o1 = __shfl_sync(0xffffffffu, end, sel);
+                pos = __shfl_sync(0xffffffffu, at, sel);
+                break;
+            }
+            lo += sel * step;
             hi = min(hi, lo + step);
         }
-        b = lo;
-        o0 = p.offsets[b];
-        const int o1 = p.offsets[b + 1];
         if (o0 < 0 || o1 < o0 || o1 > p.n_tokens) return false;
         n = o1 - o0;
-        const long long first = (long long)o0 / 64 + 2ll * b;
-        if (x < first) return false;
-        ord = (int)(x - first);
+        ord = (int)(x - ((long long)o0 / 64 + 2ll * b));
     } else {
         b = x;
         o0 = b;
         n = 1;
         ord = 0;
+        pos = p.positions[b];
     }
-    if (n == 0) return false;
-    const int pos = p.positions[b];
+    if (n == 0 || ord < 0) return false;
     if (pos < 0 || (long long)pos + n > (1ll << 31) - 64) {
-        if (flag && ord == 0) raise_error(p.err, kErrBadBlock);
+        if (flag && ord == 0 && b < p.B) raise_error(p.err, kErrBadBlock);
         // a run that starts before the sequence has no block of its own: its
         // rows are handed out 64 at a time so that a reader can zero them
-        if (ord * 64 >= n) return false;
-        *out = BlockRun{o0 + ord * 64, 0, min(64, n - ord * 64), -1};
+        if ((long long)ord * 64 >= n) return false;
+        *out = BlockRun{b, o0 + ord * 64, 0, min(64, n - ord * 64), -1, false};
         return true;
     }
     const int lead = pos % kBlockSize, blk = pos / kBlockSize + ord;
     const int last = (int)(((long long)pos + n - 1) / kBlockSize);
     if (blk > last) return false;
-    const int r0 = ord == 0 ? lead : 0;
-    const int r1 = min(kBlockSize, lead + n - ord * kBlockSize);
-    int phys = -1;
     const int slot = table_slot(p.vis, blk);
-    // a later block of this run takes the same ring slot
-    const bool replaced = p.vis.ring > 0 && slot >= ring_base(p.vis) && blk + p.vis.ring <= last;
-    if (slot >= 0 && slot < p.max_blocks && !replaced) {
-        phys = p.block_table[(size_t)b * p.max_blocks + slot];
+    *out = BlockRun{b,
+                    o0 + (ord == 0 ? 0 : ord * kBlockSize - lead),
+                    ord == 0 ? lead : 0,
+                    min(kBlockSize, lead + n - ord * kBlockSize),
+                    slot < p.max_blocks ? slot : -1,
+                    p.vis.ring > 0 && slot >= ring_base(p.vis) && blk + p.vis.ring <= last};
+    return true;
+}
+
+// Physical block of a part, -1 where there is none.  A reader reports replaced
+// blocks too; a writer just leaves them out.
+__device__ __forceinline__ int run_block(const KvRunParams &p, const BlockRun &br, bool flag,
+                                         bool reading) {
+    int phys = -1;
+    if (br.slot >= 0 && !br.replaced) {
+        phys = p.block_table[(size_t)br.b * p.max_blocks + br.slot];
         if (phys < 0 || phys >= p.num_blocks) phys = -1;
     }
-    if (phys < 0 && flag && (reading || !replaced)) raise_error(p.err, kErrBadBlock);
-    *out = BlockRun{o0 + (ord == 0 ? 0 : ord * kBlockSize - lead), r0, r1, phys};
-    return true;
+    if (phys < 0 && flag && br.b < p.B && (reading || !br.replaced))
+        raise_error(p.err, kErrBadBlock);
+    return phys;
 }
 
 // Smallest power of two s >= 2^-126 with amax <= 448 s; 0 for amax = 0.
@@ -105,106 +132,100 @@ __device__ __forceinline__ float finite_abs(float x) {
     return a <= 3.402823466e38f ? a : 0.f;        // infinities and NaN: 0
 }
 
-// 16 consecutive input values.
-template <typename T> struct In16;
-template <> struct In16<__nv_bfloat16> {
-    uint4 v[2];
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-        v[0] = __ldg(reinterpret_cast<const uint4 *>(p));
-        v[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
-    }
-    __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float *f) const {
-        Chunk<__nv_bfloat16>::unpack(v[0], f);
-        Chunk<__nv_bfloat16>::unpack(v[1], f + 8);
-    }
+// Input values of a 16-byte chunk, and the codes made of them.
+template <typename T> struct In;
+template <> struct In<__nv_bfloat16> {
+    static constexpr int kE = 8;
+    using Codes = uint2;
 };
-template <> struct In16<float> {
-    uint4 v[4];
-    __device__ __forceinline__ void load(const float *p) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ __forceinline__ void get(float *f) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) Chunk<float>::unpack(v[i], f + 4 * i);
-    }
+template <> struct In<float> {
+    static constexpr int kE = 4;
+    using Codes = uint32_t;
 };
 
-// 16 values times `by` as E4M3 codes: nearest even, saturated, NaN kept.
-__device__ __forceinline__ uint4 to_codes(const float *f, float by) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-            make_float2(f[4 * i] * by, f[4 * i + 1] * by), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-            make_float2(f[4 * i + 2] * by, f[4 * i + 3] * by), __NV_SATFINITE, __NV_E4M3);
-        w[i] = lo | (hi << 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+// Values times `by` as E4M3 codes: nearest even, saturated, NaN kept.
+__device__ __forceinline__ uint32_t four_codes(const float *f, float by) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0] * by, f[1] * by),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2] * by, f[3] * by),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+__device__ __forceinline__ void to_codes(const float *f, float by, uint2 *c) {
+    *c = make_uint2(four_codes(f, by), four_codes(f + 4, by));
+}
+__device__ __forceinline__ void to_codes(const float *f, float by, uint32_t *c) {
+    *c = four_codes(f, by);
 }
 
-// The numbers that 16 codes are (every E4M3 number is an f16 number).
-__device__ __forceinline__ void from_codes(const uint4 &c, float *f) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+// The numbers that codes are (every E4M3 number is an f16 number).
+__device__ __forceinline__ void four_values(uint32_t w, float *f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-            (__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+    for (int i = 0; i < 2; ++i) {
+        const __half2_raw h =
+            __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
         const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
         f[2 * i] = x.x;
         f[2 * i + 1] = x.y;
     }
 }
+__device__ __forceinline__ void from_codes(const uint2 &c, float *f) {
+    four_values(c.x, f);
+    four_values(c.y, f + 4);
+}
+__device__ __forceinline__ void from_codes(const uint32_t &c, float *f) { four_values(c, f); }
 
-// D threads; thread t takes 16 values of rows t / (D / 16) + 16 k, k < 4.
+// Thread t takes one 16-byte chunk of input rows t / (D / kE) + kRows k.
 template <typename T, int D>
-__global__ void __launch_bounds__(D) kv_append_fp8_block_kernel(const KvAppendBlockParams p) {
-    constexpr int kTpr = D / 16, kRows = D / kTpr, kPasses = kBlockSize / kRows;
-    __shared__ float s_max[D / 32];
+__global__ void __launch_bounds__(kRunThreads)
+kv_append_fp8_block_kernel(const KvAppendBlockParams p) {
+    constexpr int kE = In<T>::kE, kTpr = D / kE, kRows = kRunThreads / kTpr;
+    constexpr int kPasses = kBlockSize / kRows;
+    using Codes = typename In<T>::Codes;
+    __shared__ float s_max[kRunThreads / 32];
     const int tid = threadIdx.x, h = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
+    pdl_wait_primary();
+    pdl_launch_dependents();
     BlockRun br;
-    if (!locate_run(p.run, blockIdx.x, tid == 0 && h == 0 && !is_v, false, &br)) return;
-    if (br.phys < 0) return;
+    const bool flag = tid == 0 && h == 0 && !is_v;
+    if (!locate_run(p.run, blockIdx.x, flag, false, &br)) return;
     const T *src = static_cast<const T *>(is_v ? p.v_new : p.k_new);
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
-    const size_t tile = (size_t)br.phys * p.run.H_kv + h;
-    float *scale = (is_v ? p.v_scale : p.k_scale) + tile;
-    uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + tile * (kBlockSize * D);
-    const float held = *scale;
-    const int col = (tid % kTpr) * 16, row0 = tid / kTpr;
+    const int col = (tid % kTpr) * kE, row0 = tid / kTpr;
 
-    In16<T> x[kPasses];
-    float amax = 0.f;
+    // the inputs need the run only, not the block: their loads go out together
+    // with the table's
+    uint4 x[kPasses];
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
         const int r = row0 + kRows * k;
-        if (r >= br.r0 && r < br.r1)
-            x[k].load(src + (br.src + (r - br.r0)) * stride + h * D + col);
-        else
-            x[k].zero();
+        x[k] = r >= br.r0 && r < br.r1
+                   ? __ldg(reinterpret_cast<const uint4 *>(
+                         src + (br.src + (r - br.r0)) * stride + h * D + col))
+                   : make_uint4(0u, 0u, 0u, 0u);
     }
+    const int phys = run_block(p.run, br, flag, false);
+    if (phys < 0) return;
+    const size_t tile = (size_t)phys * p.run.H_kv + h;
+    float *scale = (is_v ? p.v_scale : p.k_scale) + tile;
+    uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + tile * (kBlockSize * D);
+    const float held = br.r0 > 0 ? *scale : 0.f;
+    float amax = 0.f;
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
-        float f[16];
-        x[k].get(f);
+        float f[kE];
+        Chunk<T>::unpack(x[k], f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(f[i]));
+        for (int i = 0; i < kE; ++i) amax = fmaxf(amax, finite_abs(f[i]));
     }
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // not negative
     if ((tid & 31) == 0) s_max[tid >> 5] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) amax = fmaxf(amax, s_max[w]);
+    for (int w = 0; w < kRunThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
 
-    const float old = br.r0 > 0 && held > 0.f ? held : 0.f;
+    const float old = held > 0.f ? held : 0.f;
     const float s = fmaxf(old, block_scale(amax));
     const float by = s > 0.f ? 1.f / s : 1.f;          // exact: a power of two
     if (br.r0 > 0 && s != old) {
@@ -214,10 +235,10 @@ __global__ void __launch_bounds__(D) kv_append_fp8_block_kernel(const KvAppendBl
         for (int k = 0; k < kPasses; ++k) {
             const int r = row0 + kRows * k;
             if (r < br.r0) {
-                uint4 *at = reinterpret_cast<uint4 *>(dst + r * D + col);
-                float f[16];
+                Codes *at = reinterpret_cast<Codes *>(dst + r * D + col);
+                float f[kE];
                 from_codes(*at, f);
-                *at = to_codes(f, ratio);
+                to_codes(f, ratio, at);
             }
         }
     }
@@ -225,90 +246,126 @@ __global__ void __launch_bounds__(D) kv_append_fp8_block_kernel(const KvAppendBl
     for (int k = 0; k < kPasses; ++k) {
         const int r = row0 + kRows * k;
         if (r >= br.r0 && r < br.r1) {
-            float f[16];
-            x[k].get(f);
-            *reinterpret_cast<uint4 *>(dst + r * D + col) = to_codes(f, by);
+            float f[kE];
+            Chunk<T>::unpack(x[k], f);
+            to_codes(f, by, reinterpret_cast<Codes *>(dst + r * D + col));
         }
     }
     if (tid == 0) *scale = s;
 }
 
-__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float *f) {
-    uint32_t w[8];
+__device__ __forceinline__ uint4 out_chunk(const float *f, __nv_bfloat16) {
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t *>(&b);
     }
-    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store16(float *p, const float *f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4 *>(p)[i] =
-            make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+__device__ __forceinline__ uint4 out_chunk(const float *f, float) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
 }
 
+// A CTA reads 1 << heads_log2 heads of a block; a thread keeps to one head and
+// one 16-byte chunk of the output row, so that its scale stays in a register
+// and neighbours write neighbouring chunks.
 template <typename T, int D>
-__global__ void __launch_bounds__(D) kv_read_fp8_block_kernel(const KvReadBlockParams p) {
-    constexpr int kTpr = D / 16, kRows = D / kTpr, kPasses = kBlockSize / kRows;
-    const int tid = threadIdx.x, h = blockIdx.y;
+__global__ void __launch_bounds__(kRunThreads)
+kv_read_fp8_block_kernel(const KvReadBlockParams p, int heads_log2) {
+    constexpr int kE = In<T>::kE, kTpr = D / kE, kUnits = kRunThreads / kTpr;
+    constexpr int kAhead = 4;
+    using Codes = typename In<T>::Codes;
+    const int tid = threadIdx.x, unit = tid / kTpr;
+    const int h = (blockIdx.y << heads_log2) + (unit & ((1 << heads_log2) - 1));
+    const int col = (tid % kTpr) * kE, row0 = unit >> heads_log2, rows = kUnits >> heads_log2;
     const bool is_v = blockIdx.z != 0;
-    BlockRun br;
-    if (!locate_run(p.run, blockIdx.x, tid == 0 && h == 0 && !is_v, true, &br)) return;
-    const bool gone = br.phys < 0;
-    const size_t tile = (size_t)(gone ? 0 : br.phys) * p.run.H_kv + h;
-    const float s = gone ? 0.f : (is_v ? p.v_scale : p.k_scale)[tile];
-    const uint8_t *src = (is_v ? p.v_cache : p.k_cache) + tile * (kBlockSize * D);
-    T *dst = static_cast<T *>(is_v ? p.v_out : p.k_out);
-    const int col = (tid % kTpr) * 16, row0 = tid / kTpr;
-    uint4 c[kPasses];
-#pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-        const int r = row0 + kRows * k;
-        c[k] = !gone && r >= br.r0 && r < br.r1
-                   ? __ldg(reinterpret_cast<const uint4 *>(src + r * D + col))
-                   : make_uint4(0u, 0u, 0u, 0u);
+    const size_t pitch = (size_t)p.run.H_kv * D;
+    T *dst = static_cast<T *>(is_v ? p.v_out : p.k_out) + (size_t)h * D + col;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (p.zero_rest && p.run.offsets && blockIdx.x == 0) {
+        const int n = min(p.run.offsets[0], p.run.n_tokens);        // rows before the first
+        for (int r = row0; r < n; r += rows)
+            *reinterpret_cast<uint4 *>(dst + r * pitch) = make_uint4(0u, 0u, 0u, 0u);
     }
+    BlockRun br;
+    const bool flag = tid == 0 && blockIdx.y == 0 && !is_v;
+    if (!locate_run(p.run, blockIdx.x, flag, p.zero_rest, &br)) return;
+    const int phys = run_block(p.run, br, flag, true);
+    dst += ((int64_t)br.src - br.r0) * (int64_t)pitch;
+    if (phys < 0) {
+        for (int r = br.r0 + row0; r < br.r1; r += rows)
+            *reinterpret_cast<uint4 *>(dst + r * pitch) = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    const size_t tile = (size_t)phys * p.run.H_kv + h;
+    const float s = (is_v ? p.v_scale : p.k_scale)[tile];
+    const uint8_t *src = (is_v ? p.v_cache : p.k_cache) + tile * (kBlockSize * D) + col;
+    for (int r = br.r0 + row0; r < br.r1; r += kAhead * rows) {
+        Codes c[kAhead];
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-        const int r = row0 + kRows * k;
-        if (r < br.r0 || r >= br.r1) continue;
-        float f[16];
-        from_codes(c[k], f);
+        for (int k = 0; k < kAhead; ++k)
+            if (r + k * rows < br.r1)
+                c[k] = __ldg(reinterpret_cast<const Codes *>(src + (r + k * rows) * D));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] *= s;
-        store16(dst + ((size_t)(br.src + (r - br.r0)) * p.run.H_kv + h) * D + col, f);
+        for (int k = 0; k < kAhead; ++k) {
+            if (r + k * rows >= br.r1) break;
+            float f[kE];
+            from_codes(c[k], f);
+#pragma unroll
+            for (int i = 0; i < kE; ++i) f[i] *= s;
+            *reinterpret_cast<uint4 *>(dst + (r + k * rows) * pitch) = out_chunk(f, T());
+        }
     }
 }
 
 namespace {
 
-// CTA columns: one per sequence without offsets, else the last sequence's end
-// (see locate_run).
-dim3 run_grid(const KvRunParams &r) {
-    const long long cols = r.offsets ? (long long)r.n_tokens / 64 + 2ll * r.B : r.B;
-    return dim3((unsigned)cols, (unsigned)r.H_kv, 2u);
+// CTA columns: one per sequence without offsets, else to the end of the last
+// sequence (see locate_run), and of the rows behind it.
+unsigned run_columns(const KvRunParams &r, bool rest) {
+    return (unsigned)(r.offsets ? (long long)r.n_tokens / 64 + 2ll * r.B + (rest ? 1 : 0) : r.B);
+}
+
+// Programmatic launch: the kernels wait for what came before themselves, and
+// what comes next may be set up while they run.
+template <typename K, typename... A>
+cudaError_t launch_run(K kernel, dim3 grid, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kRunThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename T>
-void append_d(const KvAppendBlockParams &p, int d, cudaStream_t s) {
-    const dim3 g = run_grid(p.run);
+cudaError_t append_d(const KvAppendBlockParams &p, int d, cudaStream_t s) {
+    const dim3 g(run_columns(p.run, false), (unsigned)p.run.H_kv, 2u);
     switch (d) {
-        case 64: kv_append_fp8_block_kernel<T, 64><<<g, 64, 0, s>>>(p); break;
-        case 128: kv_append_fp8_block_kernel<T, 128><<<g, 128, 0, s>>>(p); break;
-        default: kv_append_fp8_block_kernel<T, 256><<<g, 256, 0, s>>>(p); break;
+        case 64: return launch_run(kv_append_fp8_block_kernel<T, 64>, g, s, p);
+        case 128: return launch_run(kv_append_fp8_block_kernel<T, 128>, g, s, p);
+        default: return launch_run(kv_append_fp8_block_kernel<T, 256>, g, s, p);
     }
 }
 
 template <typename T>
-void read_d(const KvReadBlockParams &p, int d, cudaStream_t s) {
-    const dim3 g = run_grid(p.run);
+cudaError_t read_d(const KvReadBlockParams &p, int d, cudaStream_t s) {
+    // Heads of a CTA: the largest power of two that divides them, up to 32 KB
+    // of codes, so that finding the rows is paid once for many.
+    int lg = 0;
+    while ((2 << lg) * kBlockSize * d <= 32768 && p.run.H_kv % (2 << lg) == 0) ++lg;
+    const dim3 g(run_columns(p.run, p.zero_rest), (unsigned)(p.run.H_kv >> lg), 2u);
     switch (d) {
-        case 64: kv_read_fp8_block_kernel<T, 64><<<g, 64, 0, s>>>(p); break;
-        case 128: kv_read_fp8_block_kernel<T, 128><<<g, 128, 0, s>>>(p); break;
-        default: kv_read_fp8_block_kernel<T, 256><<<g, 256, 0, s>>>(p); break;
+        case 64: return launch_run(kv_read_fp8_block_kernel<T, 64>, g, s, p, lg);
+        case 128: return launch_run(kv_read_fp8_block_kernel<T, 128>, g, s, p, lg);
+        default: return launch_run(kv_read_fp8_block_kernel<T, 256>, g, s, p, lg);
     }
 }
 
@@ -316,20 +373,12 @@ void read_d(const KvReadBlockParams &p, int d, cudaStream_t s) {
 
 cudaError_t launch_kv_append_fp8_block(const KvAppendBlockParams &p, int d, bool bf16,
                                        cudaStream_t stream) {
-    if (bf16)
-        append_d<__nv_bfloat16>(p, d, stream);
-    else
-        append_d<float>(p, d, stream);
-    return cudaGetLastError();
+    return bf16 ? append_d<__nv_bfloat16>(p, d, stream) : append_d<float>(p, d, stream);
 }
 
 cudaError_t launch_kv_read_fp8_block(const KvReadBlockParams &p, int d, bool bf16,
                                      cudaStream_t stream) {
-    if (bf16)
-        read_d<__nv_bfloat16>(p, d, stream);
-    else
-        read_d<float>(p, d, stream);
-    return cudaGetLastError();
+    return bf16 ? read_d<__nv_bfloat16>(p, d, stream) : read_d<float>(p, d, stream);
 }
 
 }  // namespace attn

@@ -469,14 +469,15 @@ int kv_append_fp8_block(const void *k_new, const void *v_new, int64_t k_stride, 
  * checks).  Arguments as for kv_append_fp8_block.  Positions that the table
  * row cannot name, whose block id is outside the pool, or whose ring slot a
  * later position of the same run holds, read as zeros and are flagged
- * (ATTN_ERR_BAD_BLOCK).  Output rows that belong to no sequence are left as
- * they were.  Allocates nothing.
+ * (ATTN_ERR_BAD_BLOCK).  Output rows that belong to no sequence (before
+ * offsets[0], behind offsets[B]) are left as they were, or with zero_rest set
+ * to zeros; after bad offsets, any.  Allocates nothing.
  */
 int kv_read_fp8_block(const void *k_cache, const void *v_cache, const float *k_scale,
                       const float *v_scale, const int32_t *positions, const int32_t *offsets,
                       const int32_t *block_table, void *k_out, void *v_out, int B, int n_tokens,
                       int H_kv, int d, int max_blocks_per_seq, int num_blocks, int dtype,
-                      const attn_visibility *visibility, void *stream);
+                      int zero_rest, const attn_visibility *visibility, void *stream);
 
 /*
  * attn_decode_gqa_fp8_block -- decode attention over the block-scaled fp8

@@ -65,7 +65,7 @@ def test_append_of_nothing_launches_nothing():
 def _read(**over):
     a = dict(k_cache=P, v_cache=P, k_scale=P, v_scale=P, positions=P, offsets=P, block_table=P,
              k_out=P, v_out=P, B=1, n_tokens=0, H_kv=2, d=128, max_blocks=1, num_blocks=1,
-             dtype=attn.F32, vis=None, stream=N)
+             dtype=attn.F32, zero_rest=0, vis=None, stream=N)
     a.update(over)
     return attn.load().kv_read_fp8_block(*a.values())
 
