@@ -609,7 +609,7 @@ def fp8_block_workspace(q, k_cache):
         n = load().attn_decode_gqa_fp8_block_workspace(B, L, H_q, k_cache.shape[1], d)
         if n < 0:
             raise AttnError(n, "attn_decode_gqa_fp8_block_workspace")
-        return torch.empty(n, dtype=torch.uint8, device=q.device)
+        return torch.zeros(n, dtype=torch.uint8, device=q.device)
 
 
 @_on_device

@@ -768,14 +768,18 @@ static int check_fp8_block_sizes(int B, int q_len, int H_q, int H_kv, int d) {
     return ATTN_OK;
 }
 
+static int fp8_block_ctas(const DeviceState *st) {
+    const int n = tl_num_ctas > 0 ? tl_num_ctas : st->num_sms;
+    return n < kFp8BlockMaxCtas ? n : kFp8BlockMaxCtas;
+}
+
 int64_t attn_decode_gqa_fp8_block_workspace(int B, int q_len, int H_q, int H_kv, int d) {
     int rc = check_fp8_block_sizes(B, q_len, H_q, H_kv, d);
     if (rc) return rc;
     DeviceState *st;
     rc = device_state(&st);
     if (rc) return rc;
-    const int ctas = tl_num_ctas > 0 ? tl_num_ctas : st->num_sms;
-    return fp8_block_workspace_bytes(ctas, q_len * (H_q / H_kv), d);
+    return fp8_block_workspace_bytes(fp8_block_ctas(st), q_len * (H_q / H_kv), d);
 }
 
 int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cache,
@@ -817,7 +821,7 @@ int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cac
     rc = device_state(&st);
     if (rc) return rc;
     GqaFp8BlockParams p{};
-    p.num_ctas = tl_num_ctas > 0 ? tl_num_ctas : st->num_sms;
+    p.num_ctas = fp8_block_ctas(st);
     if (workspace_bytes < fp8_block_workspace_bytes(p.num_ctas, q_len * (H_q / H_kv), d))
         return ATTN_ERR_ARG;
     p.q = static_cast<const __nv_bfloat16 *>(q);

@@ -37,9 +37,10 @@
 // warps 12-15 keep the output.  S, P and O are double-buffered.  Every wait is
 // bounded, and tensor memory always freed.
 //
-// The work is split over all SMs by visible blocks (plan.cuh); a unit cut by a
-// CTA boundary leaves fp32 partials, which a second kernel, waiting on the
-// first by programmatic launch, joins: one CTA per boundary.
+// The work is split over all SMs by visible blocks (plan.cuh).  A unit cut by
+// a CTA boundary leaves fp32 partials; the CTA that is last to leave its own
+// joins them, in the order of the splits, so that a result does not depend on
+// which one that is.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -52,7 +53,7 @@ namespace attn {
 
 constexpr int kFbThreads = 512;
 constexpr int kFbMaxStages = 8;
-constexpr int kFbWholeBlocks = 8;                     // see launch_gqa_fp8_block
+constexpr int kFbWholeBlocks = 8, kFbJoinRows = 48;   // see launch_gqa_fp8_block
 constexpr int kFbTile = 2 * kBlockSize;               // keys of a tile
 
 template <int D, int NQ>
@@ -66,7 +67,10 @@ struct FbCfg {
     static constexpr int kSlot = kFbTile * D;
     static constexpr int kQBytes = kN * D;
     static constexpr int kPBytes = kN * kFbTile;
-    static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 10 * 1024 + 1024 /*align*/;
+    // P and O^T buffers: four, so that the softmax seldom waits for the products
+    // and the output of its earlier tiles, where tensor memory has the room.
+    static constexpr int kOut = D == 256 && NQ == 32 ? 2 : 4;
+    static constexpr int kFixed = 3 * kQBytes + kOut * kPBytes + 16 * 1024 + 1024 /*align*/;
     static constexpr int kSlots = (227 * 1024 - kFixed) / kSlot;
     static constexpr int kKStages = kSlots / 2 > kFbMaxStages ? kFbMaxStages : kSlots / 2;
     static constexpr int kVStages =
@@ -74,47 +78,77 @@ struct FbCfg {
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kKStages * kSlot;
     static constexpr int kOffQ = kOffV + kVStages * kSlot;
-    static constexpr int kOffP = kOffQ + 2 * kQBytes;
-    static constexpr int kOffBar = kOffP + 2 * kPBytes;
-    static constexpr int kSmem = kOffBar + 10 * 1024 + 1024;
+    // the next unit's queries as they are in memory: [NQ][D] bf16
+    static constexpr int kOffRaw = kOffQ + 2 * kQBytes;
+    static constexpr int kOffP = kOffRaw + kQBytes;
+    static constexpr int kOffBar = kOffP + kOut * kPBytes;
+    static constexpr int kSmem = kOffBar + 16 * 1024 + 1024;
     static constexpr uint32_t kTmemS = 0, kTmemO = 2 * kN;
-    static constexpr uint32_t kTmemUsed = 2 * kN + 2 * kHalves * kN;
+    static constexpr uint32_t kTmemUsed = 2 * kN + kOut * kHalves * kN;
     static constexpr uint32_t kTmemCols =
         kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
-    // With 32 columns the softmax needs more than its even share of registers.
-    static constexpr bool kSplitRegs = NQ == 32;
-    static constexpr int kRegsLoad = 72, kRegsSoftmax = 152, kRegsOutput = 136;
-    static_assert(kRegsLoad + 2 * kRegsSoftmax + kRegsOutput <= 4 * 128, "register split");
+    // the joining of a unit uses the rings: partial sums, a weight per split and row
+    static_assert(kFbThreads * 16 + NQ * kFp8BlockMaxCtas * 4 <= kOffQ, "room for the join");
     static_assert(kKStages >= 2 && kVStages >= 2, "at least two stages per ring");
     static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kTmemUsed <= 512, "tensor memory");
 };
+
+// A tile, as the load warp tells the others: first positions of its blocks,
+// flags and the unit's running number, blocks of the CTA's range behind it.
+struct __align__(16) FbTile {
+    int pos[2], flags, left;
+};
+constexpr int kFbFirst = 1, kFbLast = 2, kFbLastPair = 4, kFbTwo = 8, kFbSegShift = 4;
+// A unit's part: sequence, its length, the window its queries have (0: none),
+// K/V head, query rows; whether the part is all of the unit.
+struct __align__(16) FbPart {
+    int b, T, window, kvh, row0, rows, whole, pad;
+};
+// Both rings hold whatever any role may still look at: the loads are at most a
+// ring ahead of the products, and those four tiles ahead of the output.
+constexpr int kFbRing = 16;
+static_assert(kFbMaxStages + 7 <= kFbRing, "records outlive their readers");
 
 template <int NQ>
 struct FbShared {
+    // With 32 columns the two softmax groups take half of the rows of every
+    // tile each, else all rows of every other tile: the code of a group stays
+    // small (32 rows in one thread took 30% misses in the instruction cache and
+    // twice the time).
+    static constexpr bool kRowSplit = NQ == 32;
+    static constexpr int kRows = kRowSplit ? 16 : NQ;        // of a softmax thread
     // In the order of the arrivals that complete them (see their set-up).
     uint64_t k_full[kFbMaxStages], k_empty[kFbMaxStages];
     uint64_t v_full[kFbMaxStages], v_empty[kFbMaxStages];
-    uint64_t q_full[2], s_full[2], o_full[2], q_empty[2], s_free[2], p_full[2], o_free[2];
-    uint64_t mma_final;
-    static constexpr int kBars = 4 * kFbMaxStages + 15;
+    uint64_t q_full[2], o_full[4], q_empty[2], s_full[2], mma_final;
+    uint64_t o_free[4], g_sync[2], s_free[2], p_full[4];
+    static constexpr int kBars = 4 * kFbMaxStages + 23;
+    alignas(16) FbTile tile[kFbRing];
+    alignas(16) FbPart part[kFbRing];
     // Per V slot and block of the tile: K scale x softmax scale (log2 units),
     // log2 of the V scale, its reciprocal, 0 where the V scale is 0.
     alignas(16) float4 info[kFbMaxStages][2];
-    alignas(16) float qsc[2][NQ];  // power-of-two scale of each query row
-    alignas(16) int row_i[2][NQ];  // query position of each row
-    alignas(16) float wmax[2][4][NQ];   // per softmax group: largest scores per warp
-    alignas(16) float2 ref[8][NQ]; // per softmax warp: reference of the weights, factor in the sum
-    alignas(16) float grow[8][NQ]; // per softmax warp: factor of the sum so far
-    alignas(16) float top[2][NQ];  // a tile's largest score (with its V scale)
-    alignas(16) float2 join[4][NQ];     // per output warp: factor of the tile, of the rest
-    // at a unit's end, per softmax group: sums of weights, what they are relative to
-    float lsum[2][2][4][NQ];
-    float ltop[2][2][NQ];
+    alignas(16) float qsc[kFbRing][NQ];    // power-of-two scale of each query row
+    alignas(16) int row_at[kFbRing][NQ];   // its position
+    // per softmax group, on even and odd turns: largest scores per warp
+    alignas(16) float wmax[2][2][4][kRows];
+    // Per softmax warp: what the weights are relative to (negative), their
+    // factor in the sum, the factor of the sum so far.
+    alignas(16) float ref[8][kRows], fac[8][kRows], grow[8][kRows];
+    alignas(16) float top[4][NQ];  // a tile's largest score (with its V scale)
+    alignas(16) float join[4][2][NQ];   // per output warp: factor of the tile, of the rest
+    // at a part's end, per softmax group that had a tile: sums of weights, what
+    // they are relative to (row split: the first group's place holds all rows)
+    float lsum[4][2][4][NQ];
+    float ltop[4][2][NQ];
+    FbCut cut[2];                  // units that this CTA shares with others
+    int joins[2];                  // whether it is the last of them
     uint32_t tmem_base;
-    int abort;
+    int abort, never;             // set when a wait gave up; stays 0
     PlanScratch plan;
 };
-static_assert(sizeof(FbShared<32>) <= 10 * 1024, "shared block");
+static_assert(sizeof(FbShared<32>) <= 16 * 1024, "shared block");
 
 // Largest of x over the warp (NaN only where every lane is NaN).
 __device__ __forceinline__ float warp_max(float x) {
@@ -179,10 +213,28 @@ __device__ __forceinline__ void fb_tmem_ld(uint32_t addr, float *v) {
     else tmem_ld16(addr, v);
 }
 
-// Waits by testing the barrier over and over: for the threads that issue the
-// products, which everything else waits on (a suspended wait wakes up some 200
-// cycles late).  Bounds and results as mbar_wait.
-__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity,
+// mbar_wait out of line: the slow half of every wait, kept out of the loops
+// (their code has to stay in the instruction cache).
+__device__ __noinline__ bool fb_wait_slow(uint64_t *bar, uint32_t parity,
+                                          unsigned long long timeout_ns, unsigned *err,
+                                          volatile int *abort) {
+    return mbar_wait(bar, parity, timeout_ns, err, abort);
+}
+
+// A warp's wait: it tests for a while (a suspended wait wakes up some 200
+// cycles late), then sleeps.  The lanes leave together.
+__device__ __forceinline__ bool fb_wait(uint64_t *bar, uint32_t parity,
+                                        const GqaFp8BlockParams &p, volatile int *abort) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    return __all_sync(0xffffffffu, fb_wait_slow(bar, parity, p.timeout_ns, p.err, abort));
+}
+
+// The same by testing the barrier over and over: for the threads that issue
+// the products, which everything else waits on (a suspended wait wakes up some
+// 200 cycles late).
+__device__ __noinline__ bool fb_poll_slow(uint64_t *bar, uint32_t parity,
                                           unsigned long long timeout_ns, unsigned *err,
                                           volatile int *abort) {
     unsigned long long t0 = 0;
@@ -226,7 +278,6 @@ struct FbWalk {
         part();
     }
     __device__ bool done() const { return rest <= 0; }
-    __device__ int tiles() const { return (len + 1) / 2; }
     __device__ bool whole() const { return len == w.nb; }
     __device__ void next() {
         rest -= len;
@@ -293,84 +344,86 @@ __device__ __forceinline__ FbUnit fb_unit(const GqaFp8BlockParams &p, int unit) 
     return u;
 }
 
-// Query rows [first, rows) in steps of `step`, one warp each, into a Q buffer:
-// row r in columns r (hi) and NQ + r (lo) of the N side, scaled so that its
-// largest value is in [128, 256).  A row with an infinity or a NaN becomes NaN.
+// 16 bytes from global to shared memory, for fb_copies_done to wait for.
+__device__ __forceinline__ void fb_copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void fb_copies_done() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+}
+
+// Starts copying a unit's query rows first, first + step, ...; one warp.
+template <int D>
+__device__ __forceinline__ void fb_fetch_q(const GqaFp8BlockParams &p, int b, const FbUnit &u,
+                                           unsigned char *raw, int first, int step) {
+    constexpr int kChunks = D / 8;             // of a row, a power of two
+    constexpr int kAtOnce = kChunks < 32 ? 32 / kChunks : 1;
+    const int lane = threadIdx.x & 31;
+    for (int r = first + (lane / kChunks) * step; r < u.rows; r += kAtOnce * step) {
+        const int row = u.row0 + r, i = row / p.group, g = row - i * p.group, c = lane % kChunks;
+        fb_copy16(raw + (r * kChunks + c) * 16,
+                  p.q + ((int64_t)b * p.q_len + i) * p.q_stride +
+                      (size_t)(u.kvh * p.group + g) * D + c * 8);
+    }
+}
+
+// The rows that this warp copied to `raw` into a Q buffer: row r in columns r
+// (hi) and NQ + r (lo) of the N side, scaled so that its largest value is in
+// [128, 256).  A row with an infinity or a NaN becomes NaN.  (Not inlined: two
+// callers, and the code that an SM has to fetch before its first tile counts.)
 template <int D, int NQ>
-__device__ __forceinline__ void fb_prepare_q(const GqaFp8BlockParams &p, int b, const FbUnit &u,
-                                             unsigned char *q_buf, float *qsc, int *row_i,
-                                             int first, int step) {
+__device__ __noinline__ void fb_prepare_q(const unsigned char *raw, unsigned char *q_buf,
+                                          float *qsc, int *row_at, int at0, int row0, int rows,
+                                          int group, int first, int step) {
     using C = FbCfg<D, NQ>;
     constexpr int kE = D / 32;                 // values of a lane
-    constexpr int kAhead = 4;                  // rows whose loads are in flight
     const int lane = threadIdx.x & 31;
-    for (int r0 = first; r0 < u.rows; r0 += kAhead * step) {
-        __nv_bfloat162 x[kAhead][kE / 2];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int r = r0 + k * step, row = u.row0 + r;
-            if (r >= u.rows) break;
-            const int i = row / p.group, g = row % p.group;
-            const __nv_bfloat162 *src = reinterpret_cast<const __nv_bfloat162 *>(
-                p.q + ((int64_t)b * p.q_len + i) * p.q_stride +
-                (size_t)(u.kvh * p.group + g) * D + lane * kE);
-            if constexpr (kE == 8) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(src);
-                x[k][0] = *reinterpret_cast<const __nv_bfloat162 *>(&v.x);
-                x[k][1] = *reinterpret_cast<const __nv_bfloat162 *>(&v.y);
-                x[k][2] = *reinterpret_cast<const __nv_bfloat162 *>(&v.z);
-                x[k][3] = *reinterpret_cast<const __nv_bfloat162 *>(&v.w);
-            } else if constexpr (kE == 4) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(src);
-                x[k][0] = *reinterpret_cast<const __nv_bfloat162 *>(&v.x);
-                x[k][1] = *reinterpret_cast<const __nv_bfloat162 *>(&v.y);
-            } else {
-                x[k][0] = *src;
-            }
+#pragma unroll 2
+    for (int r = first; r < rows; r += step) {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(raw + r * 2 * D + lane * 2 * kE);
+        uint32_t w[kE / 2], top = 0;
+        if constexpr (kE == 8) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(src);
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else if constexpr (kE == 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(src);
+            w[0] = v.x; w[1] = v.y;
+        } else {
+            w[0] = *src;
         }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int r = r0 + k * step, row = u.row0 + r;
-            if (r >= u.rows) break;
-            float f[kE];
-            uint32_t top = 0;
+        for (int j = 0; j < kE / 2; ++j)
+            top = max(top, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+        top = __reduce_max_sync(0xffffffffu, top);
+        // 2^(exponent - 7), at least the smallest normal number
+        const uint32_t e = (uint32_t)max((int)(top >> 23) - 7, 1);
+        const float s = __uint_as_float(e << 23), by = __uint_as_float((254u - e) << 23);
+        uint32_t hi[kE / 2], lo[kE / 2];
 #pragma unroll
-            for (int e = 0; e < kE / 2; ++e) {
-                f[2 * e] = __low2float(x[k][e]);
-                f[2 * e + 1] = __high2float(x[k][e]);
-            }
+        for (int j = 0; j < kE / 2; ++j) {
+            e4m3_split2(bf16lo(w[j]) * by, bf16hi(w[j]) * by, hi[j], lo[j]);
+            if (top >= 0x7F800000u) hi[j] = 0x7F7Fu;
+        }
 #pragma unroll
-            for (int e = 0; e < kE; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-            top = __reduce_max_sync(0xffffffffu, top);
-            const bool finite = top < 0x7F800000u;
-            // 2^(exponent - 7), at least the smallest normal number
-            const float s = __uint_as_float((uint32_t)max((int)(top >> 23) - 7, 1) << 23);
-            const float by = 1.f / s;
-            uint32_t hi[kE / 2], lo[kE / 2];
-#pragma unroll
-            for (int e = 0; e < kE / 2; ++e) {
-                e4m3_split2(f[2 * e] * by, f[2 * e + 1] * by, hi[e], lo[e]);
-                if (!finite) hi[e] = 0x7F7Fu;
-            }
-#pragma unroll
-            for (int piece = 0; piece < 2; ++piece) {
-                const uint32_t *c = piece ? lo : hi;
-                const int n = r + piece * NQ, byte = lane * kE;
-                int off = n * C::kRowBytes + byte % C::kRowBytes;
-                off ^= C::kRowBytes == 128 ? ((off >> 7) & 7) << 4 : ((off >> 7) & 3) << 4;
-                unsigned char *dst = q_buf + (byte / C::kRowBytes) * (C::kN * C::kRowBytes) + off;
-                if constexpr (kE == 8)
-                    *reinterpret_cast<uint2 *>(dst) =
-                        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-                else if constexpr (kE == 4)
-                    *reinterpret_cast<uint32_t *>(dst) = c[0] | (c[1] << 16);
-                else
-                    *reinterpret_cast<uint16_t *>(dst) = (uint16_t)c[0];
-            }
-            if (lane == 0) {
-                qsc[r] = s;
-                row_i[r] = row / p.group;
-            }
+        for (int piece = 0; piece < 2; ++piece) {
+            const uint32_t *c = piece ? lo : hi;
+            const int n = r + piece * NQ, byte = lane * kE;
+            int off = n * C::kRowBytes + byte % C::kRowBytes;
+            off ^= C::kRowBytes == 128 ? ((off >> 7) & 7) << 4 : ((off >> 7) & 3) << 4;
+            unsigned char *dst = q_buf + (byte / C::kRowBytes) * (C::kN * C::kRowBytes) + off;
+            if constexpr (kE == 8)
+                *reinterpret_cast<uint2 *>(dst) =
+                    make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+            else if constexpr (kE == 4)
+                *reinterpret_cast<uint32_t *>(dst) = c[0] | (c[1] << 16);
+            else
+                *reinterpret_cast<uint16_t *>(dst) = (uint16_t)c[0];
+        }
+        if (lane == 0) {
+            qsc[r] = s;
+            row_at[r] = at0 + (row0 + r) / group;
         }
     }
 }
@@ -393,6 +446,90 @@ __device__ __forceinline__ float warp_sums(float *v, int lane) {
     return x;
 }
 
+// Joins the partials of a unit, share `part` of `parts`: first a warp per row
+// turns the splits' sums and references into weights, then each thread adds up
+// four columns of a row (several threads a share of the splits each, where
+// there are few columns).
+template <int D, int NQ>
+__device__ __forceinline__ void fb_join(const GqaFp8BlockParams &p, const FbCut &cut,
+                                        unsigned char *smem, int part, int parts) {
+    constexpr int kC = D / 4, kAhead = 8;
+    const FbUnit u = fb_unit(p, cut.unit);
+    const int n = cut.last - cut.first + 1, items = u.rows * kC;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float4 *s_o = reinterpret_cast<float4 *>(smem);
+    float *s_w = reinterpret_cast<float *>(s_o + kFbThreads);         // [rows][n]
+    auto slot = [&](int k) { return (size_t)(k == 0 ? cut.slot : 2 * (cut.first + k)) * NQ; };
+    for (int q = warp; q < u.rows; q += kFbThreads / 32) {
+        float top = -INFINITY, sum = 0.f;
+        bool nan = false;
+        for (int k = lane; k < n; k += 32) {
+            const float t = __ldcg(&p.ws_ml[slot(k) + q].x);
+            nan |= t != t;
+            top = fmaxf(top, t);
+        }
+        nan = __any_sync(0xffffffffu, nan);
+        top = nan ? NAN : warp_max(top);
+        for (int k = lane; k < n; k += 32) {
+            const float2 ml = __ldcg(p.ws_ml + slot(k) + q);
+            // a split whose keys the row does not see adds nothing
+            const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+            s_w[q * n + k] = f;
+            sum = fmaf(f, ml.y, sum);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float by = sum != 0.f ? 1.f / sum : 0.f;
+        for (int k = lane; k < n; k += 32) s_w[q * n + k] *= by;
+    }
+    __syncthreads();
+    // Threads of an item: a power of two, while each still has splits to add.
+    int par = 1;
+    while (2 * par * items <= kFbThreads * parts && 2 * par < n) par *= 2;
+    const int sub = tid & (par - 1);
+    for (int it0 = part * (kFbThreads / par); it0 < items; it0 += parts * (kFbThreads / par)) {
+        const int it = it0 + tid / par;
+        const int q = it / kC, c = (it % kC) * 4;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (it < items)
+            for (int k0 = sub; k0 < n; k0 += kAhead * par) {
+                float4 v[kAhead];
+                float f[kAhead];
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {     // all loads before any use
+                    const int k = min(k0 + a * par, n - 1);
+                    v[a] = __ldcg(
+                        reinterpret_cast<const float4 *>(p.ws_o + (slot(k) + q) * D + c));
+                    f[a] = k0 + a * par < n ? s_w[q * n + k] : 0.f;
+                }
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a)
+                    if (k0 + a * par < n)
+                        o = make_float4(fmaf(f[a], v[a].x, o.x), fmaf(f[a], v[a].y, o.y),
+                                        fmaf(f[a], v[a].z, o.z), fmaf(f[a], v[a].w, o.w));
+            }
+        if (par > 1) {
+            __syncthreads();                   // the last round's are read
+            s_o[tid] = o;
+            __syncthreads();
+            if (sub == 0 && it < items)
+                for (int k = 1; k < par; ++k) {
+                    const float4 x = s_o[tid + k];
+                    o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+                }
+        }
+        if (sub == 0 && it < items) {
+            const int row = u.row0 + q, i = row / p.group, g = row % p.group;
+            __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x, o.y),
+                                   __floats2bfloat162_rn(o.z, o.w)};
+            *reinterpret_cast<uint2 *>(p.out + ((size_t)(cut.b * p.q_len + i) * p.H_q +
+                                                u.kvh * p.group + g) * D + c) =
+                *reinterpret_cast<const uint2 *>(w);
+        }
+    }
+    __syncthreads();
+}
+
 template <int D, int NQ, bool G>
 __global__ void __launch_bounds__(kFbThreads, 1)
 gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -411,14 +548,16 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
         // the barriers, one lane each: arrivals that complete a phase
         for (int i = lane; i < FbShared<NQ>::kBars; i += 32) {
             uint64_t *bar = sh->k_full + i;
-            const uint32_t count = bar == &sh->mma_final ? 2             // both issuers
-                                   : bar >= sh->s_free ? 4               // warps
-                                   : bar >= sh->q_empty ? 9    // the issuer, the softmax warps
-                                                        : 1;
+            constexpr uint32_t kWarps = FbShared<NQ>::kRowSplit ? 8 : 4;
+            const uint32_t count = bar >= sh->s_free ? kWarps        // a tile's softmax warps
+                                   : bar >= sh->o_free ? 4           // warps of a group
+                                   : bar >= sh->s_full ? 2   // the products and their issuer
+                                                       : 1;
             mbar_init(bar, count);
         }
         if (lane == 0) {
             sh->abort = 0;
+            sh->never = 0;
             tma_prefetch_map(&tm_k);
             tma_prefetch_map(&tm_v);
         }
@@ -429,9 +568,9 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
     // earlier unit's rows (their columns are never written out).
     for (int i = tid; i < 2 * C::kQBytes / 16; i += kFbThreads)
         reinterpret_cast<uint4 *>(sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid < 2 * NQ) {
-        sh->qsc[tid / NQ][tid % NQ] = 0.f;
-        sh->row_i[tid / NQ][tid % NQ] = 0;
+    for (int i = tid; i < kFbRing * NQ; i += kFbThreads) {
+        (&sh->qsc[0][0])[i] = 0.f;
+        (&sh->row_at[0][0])[i] = 0;
     }
 
     // What came before on the stream wrote the inputs.
@@ -467,116 +606,172 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
         const long long hi = works ? cta_bound(blockIdx.x + 1, W, P) : 0;
         walk.init(pa, (int)(hi - lo), sh->plan.seq, lo - sh->plan.base);
     }
-    // Table entries and scales of 32 blocks of the unit's part at a time, one
-    // per lane of warp 0; the first ones while the CTA is still setting up.
-    int my_row = 0;
-    float my_ks = 0.f, my_vs = 0.f;
-    bool my_block = false;
-    auto fetch = [&](int base) {
-        my_row = p.num_blocks * p.H_kv * kBlockSize;           // behind the pool: zeros
-        my_block = false;
-        if (base + lane < walk.len) {
-            const int phys = p.block_table[(size_t)walk.w.b * p.max_blocks +
-                                           walk.w.slot(walk.w.blk_off + base + lane)];
-            if (phys >= 0 && phys < p.num_blocks) {
-                const size_t at = (size_t)phys * p.H_kv + walk.w.unit / p.chunks;
-                my_row = (int)at * kBlockSize;
-                my_ks = p.k_scale[at];
-                my_vs = p.v_scale[at];
-                my_block = true;
-            } else {
-                raise_error(p.err, kErrBadBlock);
-            }
-        }
+    // Table entries of up to 32 blocks of the unit's part, one per lane of warp
+    // 0 (-1: none); the first ones while the CTA is still setting up.
+    auto entries = [&](int base) {
+        return base + lane < walk.len
+                   ? p.block_table[(size_t)walk.w.b * p.max_blocks +
+                                   walk.w.slot(walk.w.blk_off + base + lane)]
+                   : -1;
     };
-    if (warp == 0 && !walk.done()) fetch(0);
+    int entry = -1;
+    if (warp == 0 && !walk.done()) entry = entries(0);
+    // The first unit's queries, by all warps that have nothing else to do yet.
+    constexpr int kHelpers = kFbThreads / 32 - 3;
+    if (warp >= 3 && !walk.done())
+        fb_fetch_q<D>(p, walk.w.b, fb_unit(p, walk.w.unit), smem + C::kOffRaw, warp - 3, kHelpers);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
 
     if (warp >= 3) {
-        // The first unit's queries: all warps that have nothing else to do yet.
-        if (!walk.done())
-            fb_prepare_q<D, NQ>(p, walk.w.b, fb_unit(p, walk.w.unit), sQ, sh->qsc[0],
-                                sh->row_i[0], warp - 3, kFbThreads / 32 - 3);
-        fence_proxy_async_smem();
-        named_barrier(1, kFbThreads - 96);
+        if (!walk.done()) {
+            const FbUnit u = fb_unit(p, walk.w.unit);
+            fb_copies_done();
+            fb_prepare_q<D, NQ>(smem + C::kOffRaw, sQ, sh->qsc[0], sh->row_at[0],
+                                walk.w.T - p.q_len, u.row0, u.rows, p.group, warp - 3, kHelpers);
+            fence_proxy_async_smem();
+        }
+        named_barrier(1, kHelpers * 32);
     }
-    if (warp < 4) {
-    if constexpr (C::kSplitRegs) regs_decrease<C::kRegsLoad>();
-    if (warp == 0) {
+    if (walk.done()) {
+        // no work: nothing waits for this CTA
+        if (warp == 3 && lane < 2) sh->cut[lane] = FbCut{0, -1, 0, 0, 0};
+        if (warp == 3 && lane == 0 && p.join_kernel && (int)blockIdx.x + 1 < p.num_ctas)
+            p.ws_cut[blockIdx.x] = FbCut{0, -1, 0, 0, 0};
+    } else if (warp == 0) {
         // ============================================================ loads
         const uint64_t pol = l2_policy_evict_first();
-        int tile = 0, n_k = 0, n_v = 0;         // tiles; copies of K and V issued (lane 0)
+        int n_k = 0, n_v = 0;                   // copies of K and V issued (lane 0)
+        int tile = 0, ks = 0, vs = 0, seg = -1;
+        uint32_t k_par = 1, v_par = 1;          // of the rings' last round
         bool ok = true;
-        for (bool first = true; ok && !walk.done(); walk.next()) {
-            for (int base = 0; ok && base < walk.len; base += 32, first = false) {
-                if (!first) fetch(base);
-                for (int j = 0; ok && j < 32 && base + j < walk.len; j += 2, ++tile) {
-                    const int row0 = __shfl_sync(0xffffffffu, my_row, j);
-                    const int row1 = __shfl_sync(0xffffffffu, my_row, j + 1);
-                    const bool two = base + j + 1 < walk.len;
-                    const uint32_t bytes = (two ? 2 : 1) * kBlockSize * D;
-                    const int ks = tile % C::kKStages, vs = tile % C::kVStages;
-                    if (lane == 0) {
-                        ok = tile < C::kKStages ||
-                             mbar_wait(&sh->k_empty[ks], (uint32_t)((tile / C::kKStages - 1) & 1),
-                                       p.timeout_ns, p.err, abort_flag);
-                        if (ok) {
-                            mbar_arrive_expect_tx(&sh->k_full[ks], bytes);
-#pragma unroll
-                            for (int x = 0; x < C::kBoxes; ++x) {
-                                unsigned char *dst = sK + ks * C::kSlot + x * C::kBoxBytes;
-                                tma_load_2d(dst, &tm_k, x * C::kRowBytes, row0, &sh->k_full[ks],
-                                            pol);
-                                if (two)
-                                    tma_load_2d(dst + kBlockSize * C::kRowBytes, &tm_k,
-                                                x * C::kRowBytes, row1, &sh->k_full[ks], pol);
-                            }
-                            n_k = tile + 1;
-                            ok = tile < C::kVStages ||
-                                 mbar_wait(&sh->v_empty[vs],
-                                           (uint32_t)((tile / C::kVStages - 1) & 1), p.timeout_ns,
-                                           p.err, abort_flag);
-                        }
-                    }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) break;
-                    if (lane == j || lane == j + 1) {
-                        // A scale of 0 makes the values 0, not the weights: they
-                        // enter the sum through any other scale.
-                        const float vse = my_vs == 0.f ? 5.421010862427522e-20f /* 2^-64 */
-                                                       : my_vs;
-                        sh->info[vs][lane - j] =
-                            my_block ? make_float4(my_ks * p.scale_log2, log2f(vse), 1.f / vse,
-                                                   my_vs == 0.f ? 0.f : 1.f)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&sh->v_full[vs], bytes);
+        int base = 0, kvh = walk.w.unit / p.chunks, left = walk.rest;
+        // This lane's block of a batch: its row among the codes, its scales.
+        int row = 0;
+        float k_scale = 0.f, v_scale = 0.f;
+        bool there = false;
+        auto look_up = [&](bool wanted) {
+            row = p.num_blocks * p.H_kv * kBlockSize;           // behind the pool: zeros
+            there = wanted && entry >= 0 && entry < p.num_blocks;
+            if (there) {
+                const size_t at = (size_t)entry * p.H_kv + kvh;
+                row = (int)at * kBlockSize;
+                k_scale = p.k_scale[at];
+                v_scale = p.v_scale[at];
+            } else if (wanted) {
+                raise_error(p.err, kErrBadBlock);
+            }
+        };
+        look_up(lane < walk.len);
+        while (ok && !walk.done()) {
+            // One batch: `count` blocks, looked up.  The next one's entries are
+            // read after its first tile is under way, its scales behind its
+            // last, so that neither is waited for.
+            const int base0 = base, len = walk.len, count = min(32, len - base);
+            const int my_row = row;
+            const int my_pos = lane < count
+                                   ? walk.w.logical(walk.w.blk_off + base + lane) * kBlockSize
+                                   : 0;
+            const float my_ks = k_scale, my_vs = v_scale;
+            const bool my_block = there;
+            if (base == 0) {
+                ++seg;
+                const FbUnit u = fb_unit(p, walk.w.unit);
+                const bool global = G && global_query(p.vis, walk.w.b, walk.w.T);
+                if (lane == 0)
+                    sh->part[seg % kFbRing] =
+                        FbPart{walk.w.b, walk.w.T, global ? 0 : p.vis.window, u.kvh, u.row0,
+                               u.rows, walk.whole() ? 1 : 0, 0};
+            }
+#pragma unroll 1
+            for (int j = 0; j < count; j += 2, ++tile) {
+                const int row0 = __shfl_sync(0xffffffffu, my_row, j);
+                const int row1 = __shfl_sync(0xffffffffu, my_row, (j + 1) & 31);
+                const int pos0 = __shfl_sync(0xffffffffu, my_pos, j);
+                const int pos1 = __shfl_sync(0xffffffffu, my_pos, (j + 1) & 31);
+                const bool two = j + 1 < count;
+                const uint32_t bytes = (two ? 2 : 1) * kBlockSize * D;
+                left -= two ? 2 : 1;
+                if (lane == 0) {
+                    ok = tile < C::kKStages || mbar_test(&sh->k_empty[ks], k_par) ||
+                         fb_wait_slow(&sh->k_empty[ks], k_par, p.timeout_ns, p.err, abort_flag);
+                    if (ok) {
+                        const int at = base0 + j;
+                        sh->tile[tile % kFbRing] =
+                            FbTile{{pos0, pos1},
+                                   (two ? kFbTwo : 0) | (at == 0 ? kFbFirst : 0) | (at + 2 >= len ? kFbLast : 0) |
+                                       (at + 4 >= len ? kFbLastPair : 0) | seg << kFbSegShift,
+                                   left};
+                        mbar_arrive_expect_tx(&sh->k_full[ks], bytes);
 #pragma unroll
                         for (int x = 0; x < C::kBoxes; ++x) {
-                            unsigned char *dst = sV + vs * C::kSlot + x * C::kBoxBytes;
-                            tma_load_2d(dst, &tm_v, x * C::kRowBytes, row0, &sh->v_full[vs], pol);
+                            unsigned char *dst = sK + ks * C::kSlot + x * C::kBoxBytes;
+                            tma_load_2d(dst, &tm_k, x * C::kRowBytes, row0, &sh->k_full[ks], pol);
                             if (two)
-                                tma_load_2d(dst + kBlockSize * C::kRowBytes, &tm_v,
-                                            x * C::kRowBytes, row1, &sh->v_full[vs], pol);
+                                tma_load_2d(dst + kBlockSize * C::kRowBytes, &tm_k,
+                                            x * C::kRowBytes, row1, &sh->k_full[ks], pol);
                         }
-                        n_v = tile + 1;
+                        n_k = tile + 1;
+                        ok = tile < C::kVStages || mbar_test(&sh->v_empty[vs], v_par) ||
+                             fb_wait_slow(&sh->v_empty[vs], v_par, p.timeout_ns, p.err,
+                                          abort_flag);
                     }
                 }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if (lane == j || lane == j + 1) {
+                    // A scale of 0 makes the values 0, not the weights: they
+                    // enter the sum through any other scale.
+                    const float vse = my_vs == 0.f ? 5.421010862427522e-20f /* 2^-64 */ : my_vs;
+                    sh->info[vs][lane - j] =
+                        my_block && lane < count
+                            ? make_float4(my_ks * p.scale_log2, log2f(vse), 1.f / vse,
+                                          my_vs == 0.f ? 0.f : 1.f)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh->v_full[vs], bytes);
+#pragma unroll
+                    for (int x = 0; x < C::kBoxes; ++x) {
+                        unsigned char *dst = sV + vs * C::kSlot + x * C::kBoxBytes;
+                        tma_load_2d(dst, &tm_v, x * C::kRowBytes, row0, &sh->v_full[vs], pol);
+                        if (two)
+                            tma_load_2d(dst + kBlockSize * C::kRowBytes, &tm_v, x * C::kRowBytes,
+                                        row1, &sh->v_full[vs], pol);
+                    }
+                    n_v = tile + 1;
+                }
+                if (++ks == C::kKStages) {
+                    ks = 0;
+                    k_par ^= 1u;
+                }
+                if (++vs == C::kVStages) {
+                    vs = 0;
+                    v_par ^= 1u;
+                }
+                if (j == 0) {
+                    base += 32;
+                    if (base >= walk.len) {
+                        walk.next();
+                        base = 0;
+                        if (!walk.done()) kvh = walk.w.unit / p.chunks;
+                    }
+                    entry = walk.done() ? -1 : entries(base);
+                }
             }
+            if (ok && !walk.done()) look_up(base + lane < walk.len);
         }
         // Copies still under way must land before the CTA ends.
         if (lane == 0) {
             for (int t = max(n_k - C::kKStages, 0); t < n_k; ++t)
-                mbar_wait(&sh->k_full[t % C::kKStages], (uint32_t)((t / C::kKStages) & 1),
-                          p.timeout_ns, p.err, nullptr);
+                fb_wait_slow(&sh->k_full[t % C::kKStages], (uint32_t)((t / C::kKStages) & 1),
+                             p.timeout_ns, p.err, abort_flag + 1);
             for (int t = max(n_v - C::kVStages, 0); t < n_v; ++t)
-                mbar_wait(&sh->v_full[t % C::kVStages], (uint32_t)((t / C::kVStages) & 1),
-                          p.timeout_ns, p.err, nullptr);
+                fb_wait_slow(&sh->v_full[t % C::kVStages], (uint32_t)((t / C::kVStages) & 1),
+                             p.timeout_ns, p.err, abort_flag + 1);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -587,36 +782,40 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             constexpr int kSteps = C::kRowBytes / 32;
             const uint64_t dk = fb_desc(smem_u32(sK), 16, C::kRowBytes * 8, kLayout);
             const uint64_t dq = fb_desc(smem_u32(sQ), 16, C::kRowBytes * 8, kLayout);
-            int n = 0, seg = 0, ks = 0, turn = 0;          // slot of the ring, its round
-            bool ok = true;
-            for (; ok && !walk.done(); walk.next(), ++seg) {
-                ok = mbar_poll(&sh->q_full[seg & 1], (uint32_t)((seg >> 1) & 1), p.timeout_ns,
-                               p.err, abort_flag);
-                for (int t = walk.tiles(); ok && t > 0; --t, ++n) {
-                    ok = (n < 2 || mbar_poll(&sh->s_free[n & 1], (uint32_t)((n / 2 - 1) & 1),
-                                             p.timeout_ns, p.err, abort_flag)) &&
-                         mbar_poll(&sh->k_full[ks], (uint32_t)(turn & 1), p.timeout_ns, p.err,
-                                   abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return mbar_test(bar, parity) ||
+                       fb_poll_slow(bar, parity, p.timeout_ns, p.err, abort_flag);
+            };
+            int ks = 0;
+            uint32_t k_par = 0;
+            for (int n = 0;; ++n) {
+                if (n >= 2 && !wait(&sh->s_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) break;
+                if (!wait(&sh->k_full[ks], k_par)) break;
+                const FbTile at = sh->tile[n % kFbRing];
+                const int seg = at.flags >> kFbSegShift;
+                if ((at.flags & kFbFirst) &&
+                    !wait(&sh->q_full[seg & 1], (uint32_t)((seg >> 1) & 1)))
+                    break;
+                tc_fence_after();
 #pragma unroll
-                    for (int s = 0; s < C::kBoxes * kSteps; ++s) {
-                        const int x = s / kSteps, o = (s % kSteps) * 32;
-                        // addresses count in 16 bytes
-                        umma_f8(tmem + C::kTmemS + (n & 1) * C::kN,
-                                dk + ((ks * C::kSlot + x * C::kBoxBytes + o) >> 4),
-                                dq + (((seg & 1) * C::kQBytes + x * C::kN * C::kRowBytes + o) >>
-                                      4),
-                                idesc, s != 0);
-                    }
-                    umma_commit(&sh->s_full[n & 1]);
-                    umma_commit(&sh->k_empty[ks]);
-                    if (++ks == C::kKStages) {
-                        ks = 0;
-                        ++turn;
-                    }
+                for (int s = 0; s < C::kBoxes * kSteps; ++s) {
+                    const int x = s / kSteps, o = (s % kSteps) * 32;
+                    // addresses count in 16 bytes
+                    umma_f8(tmem + C::kTmemS + (n & 1) * C::kN,
+                            dk + ((ks * C::kSlot + x * C::kBoxBytes + o) >> 4),
+                            dq + (((seg & 1) * C::kQBytes + x * C::kN * C::kRowBytes + o) >> 4),
+                            idesc, s != 0);
                 }
-                if (ok) umma_commit(&sh->q_empty[seg & 1]);
+                umma_commit(&sh->s_full[n & 1]);
+                // what this thread has seen (the rows' scales), the softmax may too
+                mbar_arrive(&sh->s_full[n & 1]);
+                umma_commit(&sh->k_empty[ks]);
+                if (at.flags & kFbLast) umma_commit(&sh->q_empty[seg & 1]);
+                if (at.left == 0) break;
+                if (++ks == C::kKStages) {
+                    ks = 0;
+                    k_par ^= 1u;
+                }
             }
             umma_commit(&sh->mma_final);
         }
@@ -628,385 +827,401 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             constexpr int kLayout = C::kRowBytes == 128 ? 2 : 4;
             const uint64_t dv = fb_desc(smem_u32(sV), 16, C::kRowBytes * 8, kLayout);
             const uint64_t dp = fb_desc(smem_u32(sP), 128, 2048, 0);
-            int n = 0, vs = 0, turn = 0;
-            bool ok = true;
-            for (; ok && !walk.done(); walk.next()) {
-                for (int t = walk.tiles(); ok && t > 0; --t, ++n) {
-                    ok = mbar_poll(&sh->v_full[vs], (uint32_t)(turn & 1), p.timeout_ns, p.err,
-                                   abort_flag) &&
-                         (n < 2 || mbar_poll(&sh->o_free[n & 1], (uint32_t)((n / 2 - 1) & 1),
-                                             p.timeout_ns, p.err, abort_flag)) &&
-                         mbar_poll(&sh->p_full[n & 1], (uint32_t)((n >> 1) & 1), p.timeout_ns,
-                                   p.err, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return mbar_test(bar, parity) ||
+                       fb_poll_slow(bar, parity, p.timeout_ns, p.err, abort_flag);
+            };
+            int vs = 0;
+            uint32_t v_par = 0;
+            for (int n = 0;; ++n) {
+                if (!wait(&sh->v_full[vs], v_par)) break;
+                const int buf = n % C::kOut;
+                const uint32_t par = (uint32_t)((n / C::kOut) & 1);
+                if (n >= C::kOut && !wait(&sh->o_free[buf], par ^ 1u)) break;
+                if (!wait(&sh->p_full[buf], par)) break;
+                tc_fence_after();
 #pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
+                for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-                        for (int s = 0; s < kFbTile / 32; ++s)
-                            umma_f8(tmem + C::kTmemO + ((n & 1) * C::kHalves + h) * C::kN,
-                                    dv + ((vs * C::kSlot + h * C::kBoxBytes +
-                                           s * 32 * C::kRowBytes) >> 4),
-                                    dp + (((n & 1) * C::kPBytes + s * 512) >> 4), idesc, s != 0);
-                    umma_commit(&sh->o_full[n & 1]);
-                    umma_commit(&sh->v_empty[vs]);
-                    if (++vs == C::kVStages) {
-                        vs = 0;
-                        ++turn;
-                    }
+                    for (int s = 0; s < kFbTile / 32; ++s)
+                        umma_f8(tmem + C::kTmemO + (buf * C::kHalves + h) * C::kN,
+                                dv + ((vs * C::kSlot + h * C::kBoxBytes + s * 32 * C::kRowBytes) >>
+                                      4),
+                                dp + ((buf * C::kPBytes + s * 512) >> 4), idesc, s != 0);
+                const int left = sh->tile[n % kFbRing].left;
+                umma_commit(&sh->o_full[buf]);
+                umma_commit(&sh->v_empty[vs]);
+                if (left == 0) break;
+                if (++vs == C::kVStages) {
+                    vs = 0;
+                    v_par ^= 1u;
                 }
             }
             umma_commit(&sh->mma_final);
             // Both issuers' products are done before tensor memory is freed.
-            mbar_wait(&sh->mma_final, 0, p.timeout_ns, p.err, nullptr);
+            fb_wait_slow(&sh->mma_final, 0, p.timeout_ns, p.err, abort_flag + 1);
         }
         __syncwarp();
-    } else {
-            // ================================================== next queries
-            int seg = 0;
-            bool cut = false;          // the range's last unit goes on in the next CTA
-            for (; !walk.done(); ++seg) {
-                const int buf = seg & 1;
-                if (seg > 0) {
-                    const bool ok =
-                        seg < 2 || mbar_wait(&sh->q_empty[buf], (uint32_t)((seg / 2 - 1) & 1),
-                                             p.timeout_ns, p.err, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    fb_prepare_q<D, NQ>(p, walk.w.b, fb_unit(p, walk.w.unit),
-                                        sQ + buf * C::kQBytes, sh->qsc[buf], sh->row_i[buf], 0,
-                                        1);
-                    fence_proxy_async_smem();
-                }
-                mbar_arrive_warp(&sh->q_full[buf]);
-                cut = walk.w.blk_off + walk.len < walk.w.nb;
-                walk.next();
+    } else if (warp == 3) {
+        // ====================================================== next queries
+        bool ok = true;
+        if (lane < 2) sh->cut[lane] = FbCut{0, -1, 0, 0, 0};
+        __syncwarp();
+        FbCut end{0, -1, 0, 0, 0};             // of the unit cut at the range's end
+        for (int seg = 0; !walk.done(); ++seg) {
+            const int buf = seg & 1;
+            // Where a wait gives up, the walk still goes on to the range's end:
+            // other CTAs count on this one's arrival at the units it shares.
+            if (seg >= 2 && ok)
+                ok = __all_sync(0xffffffffu,
+                                fb_wait_slow(&sh->q_empty[buf], (uint32_t)((seg / 2 - 1) & 1),
+                                             p.timeout_ns, p.err, abort_flag));
+            if (seg > 0) {
+                const FbUnit u = fb_unit(p, walk.w.unit);
+                fb_copies_done();
+                fb_prepare_q<D, NQ>(smem + C::kOffRaw, sQ + buf * C::kQBytes,
+                                    sh->qsc[seg % kFbRing], sh->row_at[seg % kFbRing],
+                                    walk.w.T - p.q_len, u.row0, u.rows, p.group, 0, 1);
+                fence_proxy_async_smem();
             }
-            // What the second kernel has to join at this CTA's end: the CTAs
-            // that hold the unit, the first one's slot, sequence and unit.
-            if (!p.whole_units && lane == 0 && (int)blockIdx.x + 1 < p.num_ctas) {
-                FbCut c{0, -1, 0, 0, 0};
-                if (cut) {
-                    const int P = working_ctas(W, p.num_ctas);
-                    const long long su = cta_bound(blockIdx.x + 1, W, P) - walk.w.blk_off;
-                    c.first = cta_of(su, W, P);
-                    c.last = cta_of(su + walk.w.nb - 1, W, P);
-                    c.slot = 2 * c.first + (cta_bound(c.first, W, P) == su ? 0 : 1);
-                    c.b = walk.w.b;
-                    c.unit = walk.w.unit;
-                }
-                p.ws_cut[blockIdx.x] = c;
+            mbar_arrive_warp(&sh->q_full[buf]);
+            // A unit that begins in an earlier CTA, or goes on in the next: the
+            // CTAs that hold it, and the first one's partial.
+            if (lane == 0 && !walk.whole() && !p.whole_units) {
+                const int P = working_ctas(W, p.num_ctas);
+                // the unit's first block in the list; this part starts `rest`
+                // before the range's end
+                const long long su =
+                    cta_bound(blockIdx.x + 1, W, P) - walk.rest - walk.w.blk_off;
+                const int c0 = cta_of(su, W, P);
+                const FbCut c{c0, cta_of(su + walk.w.nb - 1, W, P),
+                              2 * c0 + (cta_bound(c0, W, P) == su ? 0 : 1), walk.w.b,
+                              walk.w.unit};
+                sh->cut[seg == 0 ? 0 : 1] = c;
+                if (walk.w.blk_off + walk.len < walk.w.nb) end = c;
             }
-    }
+            walk.next();
+            __syncwarp();
+            if (!walk.done())
+                fb_fetch_q<D>(p, walk.w.b, fb_unit(p, walk.w.unit), smem + C::kOffRaw, 0, 1);
+        }
+        if (p.join_kernel && lane == 0 && (int)blockIdx.x + 1 < p.num_ctas)
+            p.ws_cut[blockIdx.x] = end;
     } else if (warp < 12) {
-            if constexpr (C::kSplitRegs) regs_increase<C::kRegsSoftmax>();
-            // ======================================================= softmax
-            const int grp = (warp - 4) >> 2, w = warp & 3, half = w >> 1;
-            const int key = 32 * w + lane;                     // of the tile
-            const uint32_t tlane = (uint32_t)(32 * w) << 16;
-            const int L = p.q_len;
-            float2 *ref = sh->ref[warp - 4];
-            float *grow = sh->grow[warp - 4];
-            int n = 0, seg = 0;                                // n: tiles before this unit's part
-            bool ok = true;
-            // Where a wait gives up, the warp goes on without waiting: the four
-            // warps meet in a barrier at every tile, and none may miss it.
-            auto wait = [&](uint64_t *bar, int phase) {
-                if (ok && !mbar_test(bar, (uint32_t)(phase & 1)))
-                    ok = mbar_wait(bar, (uint32_t)(phase & 1), p.timeout_ns, p.err, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-            };
-            for (; !walk.done(); n += walk.tiles(), walk.next(), ++seg) {
-                const int T = walk.w.T, tiles = walk.tiles();
-                const bool global = G && global_query(p.vis, walk.w.b, T);
-                const int window = global ? 0 : p.vis.window, sink = p.vis.sink;
-                float2 l[NQ / 2];
-                float top = -INFINITY;                         // of row `lane`
-#pragma unroll
-                for (int q = 0; q < NQ / 2; ++q) l[q] = make_float2(0.f, 0.f);
-                wait(&sh->q_full[seg & 1], seg >> 1);
-                const float *qsc = sh->qsc[seg & 1];
-                for (int t = (n & 1) ^ grp; t < tiles; t += 2) {
-                    const int at_tile = n + t, round = at_tile >> 1;
-                    const int vs = at_tile % C::kVStages;
-                    const bool there = 2 * t + half < walk.len;     // this warp's block
-                    const int blk = walk.w.logical(walk.w.blk_off + 2 * t + (there ? half : 0));
-                    const int first = blk * kBlockSize + 32 * (w & 1), pos = first + lane;
-                    unsigned long long gmask = 0ull;
-                    if (G && window > 0 && first <= T - 1 - window)
-                        gmask = global_mask(p.vis, walk.w.b, blk, lane);
-                    // every key of the warp seen by every query
-                    const bool all = there && first + 31 <= T - L &&
-                                     (window <= 0 || first > T - 1 - window || first + 31 < sink);
-                    wait(&sh->v_full[vs], at_tile / C::kVStages);
-                    const float4 info = sh->info[vs][half];
-                    if (!all || info.w == 0.f) {
-                        // Rows that no query sees may hold NaN codes: they are
-                        // zeroed, since 0 x NaN would reach every row's sum.  So
-                        // are those whose scale is 0.
-                        const bool any = there && pos < T && info.w != 0.f &&
-                                         (window <= 0 || pos > T - L - window || pos < sink ||
-                                          ((gmask >> (pos & 63)) & 1ull));
-                        if (!any) {
-                            unsigned char *v = sV + vs * C::kSlot + key * C::kRowBytes;
-#pragma unroll
-                            for (int x = 0; x < C::kBoxes; ++x)
-#pragma unroll
-                                for (int c = 0; c < C::kRowBytes / 16; ++c)
-                                    reinterpret_cast<uint4 *>(v + x * C::kBoxBytes)[c] =
-                                        make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                    wait(&sh->s_full[grp], round);
-                    tc_fence_after();
-                    float2 s[NQ / 2];
-                    {
-                        float x[NQ], y[NQ];
-                        const uint32_t at = tmem + C::kTmemS + grp * C::kN + tlane;
-                        if constexpr (NQ == 8) {
-                            float xy[16];
-                            tmem_ld16(at, xy);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                x[q] = xy[q];
-                                y[q] = xy[8 + q];
-                            }
-                        } else {
-                            fb_tmem_ld<NQ>(at, x);
-                            fb_tmem_ld<NQ>(at + NQ, y);
-                        }
-                        tc_fence_before();
-                        mbar_arrive_warp(&sh->s_free[grp]);
-                        // scores in log2 units, the V scale's exponent among them
-                        const float2 k2 = make_float2(info.x, info.x);
-                        const float2 v2 = make_float2(info.y, info.y);
-                        const float2 part = make_float2(0.03125f, 0.03125f);
-#pragma unroll
-                        for (int q = 0; q < NQ; q += 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(qsc + q);
-                            s[q / 2] = __ffma2_rn(
-                                __ffma2_rn(make_float2(y[q], y[q + 1]), part,
-                                           make_float2(x[q], x[q + 1])),
-                                __fmul2_rn(make_float2(f.x, f.y), k2), v2);
-                            s[q / 2 + 1] = __ffma2_rn(
-                                __ffma2_rn(make_float2(y[q + 2], y[q + 3]), part,
-                                           make_float2(x[q + 2], x[q + 3])),
-                                __fmul2_rn(make_float2(f.z, f.w), k2), v2);
-                        }
-                    }
-                    if (!all) {
-                        auto seen = [&](int q) {
-                            const int at = T - L + (L > 1 ? sh->row_i[seg & 1][q] : 0);
-                            return there && pos <= at &&
-                                   (window <= 0 || pos > at - window || pos < sink ||
-                                    ((gmask >> (pos & 63)) & 1ull));
-                        };
-#pragma unroll
-                        for (int q = 0; q < NQ; q += 2) {
-                            if (!seen(q)) s[q / 2].x = -INFINITY;
-                            if (!seen(q + 1)) s[q / 2].y = -INFINITY;
-                        }
-                    }
-                    // largest of the tile, per row
-                    {
-                        float mine = 0.f;
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            const float m = warp_max(q & 1 ? s[q / 2].y : s[q / 2].x);
-                            if (lane == q) mine = m;
-                        }
-                        // The P buffer and what goes with it are free again: the
-                        // group's last tile is through, wmax read by all.
-                        if (round >= 1) wait(&sh->o_free[grp], round - 1);
-                        if (lane < NQ) sh->wmax[grp][w][lane] = mine;
-                    }
-                    named_barrier(2 + grp, 128);
-                    bool grew = false;
-                    if (lane < NQ) {
-                        const float m = fmaxf(fmaxf(sh->wmax[grp][0][lane], sh->wmax[grp][1][lane]),
-                                              fmaxf(sh->wmax[grp][2][lane],
-                                                    sh->wmax[grp][3][lane]));
-                        const float now = m != m ? m : fmaxf(top, m);
-                        // factor of this tile's weights (2^8 in them) in the sum
-                        const float c = m == -INFINITY ? 0.f : exp2_approx(m - now - 8.f);
-                        const float a = top == now ? 1.f : exp2_approx(top - now);
-                        ref[lane] = make_float2(m == -INFINITY ? 0.f : 8.f - m, c * info.z);
-                        grow[lane] = a;
-                        grew = a != 1.f;
-                        top = now;
-                        if (w == 0) sh->top[grp][lane] = m;
-                    }
-                    grew = __any_sync(0xffffffffu, grew);
-                    __syncwarp();
-                    if (grew) {
-#pragma unroll
-                        for (int q = 0; q < NQ; q += 2)
-                            l[q / 2] = __fmul2_rn(l[q / 2],
-                                                  *reinterpret_cast<const float2 *>(grow + q));
-                    }
-                    uint32_t hi[NQ / 4], lo[NQ / 4];
-#pragma unroll
-                    for (int q = 0; q < NQ; q += 2) {
-                        const float4 r = *reinterpret_cast<const float4 *>(&ref[q]);
-                        float2 x = __fadd2_rn(s[q / 2], make_float2(r.x, r.z));
-                        x.x = exp2_approx(x.x);
-                        x.y = exp2_approx(x.y);
-                        l[q / 2] = __ffma2_rn(x, make_float2(r.y, r.w), l[q / 2]);
-                        uint32_t h2, l2;
-                        e4m3_split2(x.x, x.y, h2, l2);
-                        if (q % 4 == 0) {
-                            hi[q / 4] = h2;
-                            lo[q / 4] = l2;
-                        } else {
-                            hi[q / 4] |= h2 << 16;
-                            lo[q / 4] |= l2 << 16;
-                        }
-                    }
-                    // 16 columns of a key are 16 bytes, keys one after another
-                    unsigned char *pk = sP + grp * C::kPBytes + key * 16;
-                    if constexpr (NQ == 8) {
-                        *reinterpret_cast<uint4 *>(pk) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-                    } else {
-#pragma unroll
-                        for (int g = 0; g < NQ / 16; ++g) {
-                            *reinterpret_cast<uint4 *>(pk + g * 2048) = make_uint4(
-                                hi[4 * g], hi[4 * g + 1], hi[4 * g + 2], hi[4 * g + 3]);
-                            *reinterpret_cast<uint4 *>(pk + (NQ / 16 + g) * 2048) = make_uint4(
-                                lo[4 * g], lo[4 * g + 1], lo[4 * g + 2], lo[4 * g + 3]);
-                        }
-                    }
-                    if (t + 2 >= tiles) {              // the group's last of the unit
-                        float v[NQ];
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) v[q] = q & 1 ? l[q / 2].y : l[q / 2].x;
-                        const float sum = warp_sums<NQ>(v, lane);
-                        if (lane < NQ) {
-                            sh->lsum[seg & 1][grp][w][lane] = sum;
-                            if (w == 0) sh->ltop[seg & 1][grp][lane] = top;
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive_warp(&sh->p_full[grp]);
+        // ========================================================== softmax
+        constexpr bool kSplit = FbShared<NQ>::kRowSplit;
+        constexpr int R = FbShared<NQ>::kRows;                 // rows of a thread
+        constexpr int kStep = kSplit ? 1 : 2;                  // tiles from one to the next
+        const int grp = (warp - 4) >> 2, w = warp & 3, half = w >> 1;
+        const int q0 = kSplit ? R * grp : 0;                   // first row
+        const int key = 32 * w + lane;                         // of the tile
+        const uint32_t tlane = (uint32_t)(32 * w) << 16;
+        const int L = p.q_len, sink = p.vis.sink;
+        float *ref = sh->ref[warp - 4], *fac = sh->fac[warp - 4], *grow = sh->grow[warp - 4];
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return fb_wait(bar, parity, p, abort_flag);
+        };
+        float2 l[R / 2];
+        float top = -INFINITY;                                 // of row q0 + lane
+        int seg = -1, turns = 0;                               // tiles of this group so far
+        for (int n = kSplit ? 0 : grp, left = walk.rest;; n += kStep, ++turns) {
+            if (!kSplit && n > 0) {
+                // Whether there is a tile n: one block behind tile n - 2 is
+                // tile n - 1; two may be one tile or two.
+                if (left <= 1) break;
+                if (left == 2) {
+                    const int o = n - 1;
+                    if (!wait(&sh->v_full[o % C::kVStages], (uint32_t)((o / C::kVStages) & 1)))
+                        break;
+                    if (sh->tile[o % kFbRing].left == 0) break;
                 }
-                mbar_arrive_warp(&sh->q_empty[seg & 1]);
             }
+            const int buf = n & 1, vs = n % C::kVStages, ob = n % C::kOut;
+            if (!wait(&sh->v_full[vs], (uint32_t)((n / C::kVStages) & 1))) break;
+            const FbTile tile = sh->tile[n % kFbRing];
+            const float4 info = sh->info[vs][half];
+            left = tile.left;
+            if ((tile.flags >> kFbSegShift) != seg) {
+                seg = tile.flags >> kFbSegShift;
+                top = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < R / 2; ++q) l[q] = make_float2(0.f, 0.f);
+            }
+            const FbPart &part = sh->part[seg % kFbRing];
+            const int T = part.T, window = part.window;
+            const int first = (half ? tile.pos[1] : tile.pos[0]) + 32 * (w & 1);
+            const int pos = first + lane;
+            const bool there = half == 0 || (tile.flags & kFbTwo);   // this warp's block
+            // every key of the warp seen by every query
+            const bool all = there && first + 31 <= T - L &&
+                             (window <= 0 || first > T - 1 - window || first + 31 < sink);
+            bool early = window <= 0 || pos < sink;             // whatever the window
+            if (!all || info.w == 0.f) {
+                if (G && there && window > 0 && first <= T - 1 - window)
+                    early |= (global_mask(p.vis, part.b, first / kBlockSize, lane) >> (pos & 63)) &
+                             1ull;
+                // Rows that no query sees may hold NaN codes: they are zeroed,
+                // since 0 x NaN would reach every row's sum.  So are those whose
+                // scale is 0.  (Row split: either group zeroes half of a row.)
+                if (!(there && pos < T && info.w != 0.f && (early || pos > T - L - window))) {
+                    constexpr int kZero = C::kRowBytes / 16 / (kSplit ? 2 : 1);
+                    uint4 *v = reinterpret_cast<uint4 *>(sV + vs * C::kSlot +
+                                                         key * C::kRowBytes) +
+                               (kSplit ? grp * kZero : 0);
+#pragma unroll
+                    for (int x = 0; x < C::kBoxes; ++x)
+#pragma unroll
+                        for (int c = 0; c < kZero; ++c)
+                            v[x * (C::kBoxBytes / 16) + c] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            if (!wait(&sh->s_full[buf], (uint32_t)((n >> 1) & 1))) break;
+            tc_fence_after();
+            float2 s[R / 2];
+            {
+                float x[2 * R];
+                const uint32_t at = tmem + C::kTmemS + buf * C::kN + q0 + tlane;
+                if constexpr (!kSplit) {
+                    fb_tmem_ld<2 * R>(at, x);
+                } else {
+                    fb_tmem_ld<R>(at, x);
+                    fb_tmem_ld<R>(at + NQ, x + R);
+                }
+                tc_fence_before();
+                mbar_arrive_warp(&sh->s_free[buf]);
+                // scores in log2 units, the V scale's exponent among them
+                const float2 k2 = make_float2(info.x, info.x);
+                const float2 v2 = make_float2(info.y, info.y);
+                const float2 piece = make_float2(0.03125f, 0.03125f);
+                const float *qsc = &sh->qsc[seg % kFbRing][q0], *y = x + R;
+#pragma unroll
+                for (int q = 0; q < R; q += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(qsc + q);
+                    s[q / 2] = __ffma2_rn(__ffma2_rn(make_float2(y[q], y[q + 1]), piece,
+                                                     make_float2(x[q], x[q + 1])),
+                                          __fmul2_rn(make_float2(f.x, f.y), k2), v2);
+                    s[q / 2 + 1] = __ffma2_rn(__ffma2_rn(make_float2(y[q + 2], y[q + 3]), piece,
+                                                         make_float2(x[q + 2], x[q + 3])),
+                                              __fmul2_rn(make_float2(f.z, f.w), k2), v2);
+                }
+            }
+            if (!all) {
+                // a row at position `at` sees the `span` positions up to it
+                const unsigned span = !there ? 0u : early ? 1u << 31 : (unsigned)window;
+                const int *row_at = &sh->row_at[seg % kFbRing][q0];
+#pragma unroll
+                for (int q = 0; q < R; q += 4) {
+                    const int4 at = *reinterpret_cast<const int4 *>(row_at + q);
+                    if ((unsigned)(at.x - pos) >= span) s[q / 2].x = -INFINITY;
+                    if ((unsigned)(at.y - pos) >= span) s[q / 2].y = -INFINITY;
+                    if ((unsigned)(at.z - pos) >= span) s[q / 2 + 1].x = -INFINITY;
+                    if ((unsigned)(at.w - pos) >= span) s[q / 2 + 1].y = -INFINITY;
+                }
+            }
+            // largest of the tile, per row (every lane has it: one writes)
+            {
+                float m[R];
+#pragma unroll
+                for (int q = 0; q < R; q += 2) {
+                    m[q] = warp_max(s[q / 2].x);
+                    m[q + 1] = warp_max(s[q / 2].y);
+                }
+                if (lane == 0) {
+#pragma unroll
+                    for (int q = 0; q < R; q += 4)
+                        *reinterpret_cast<float4 *>(&sh->wmax[grp][turns & 1][w][q]) =
+                            make_float4(m[q], m[q + 1], m[q + 2], m[q + 3]);
+                }
+            }
+            mbar_arrive_warp(&sh->g_sync[grp]);
+            if (!wait(&sh->g_sync[grp], (uint32_t)(turns & 1))) break;
+            // the P buffer, and what goes with it, is free again
+            if (n >= C::kOut && !wait(&sh->o_free[ob], (uint32_t)((n / C::kOut - 1) & 1))) break;
+            bool grew = false;
+            if (lane < R) {
+                const float(*wm)[R] = sh->wmax[grp][turns & 1];
+                const float m =
+                    fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
+                const float now = m != m ? m : fmaxf(top, m);
+                // factor of this tile's weights (2^8 in them) in the sum
+                const float c = m == -INFINITY ? 0.f : exp2_approx(m - now - 8.f);
+                const float a = top == now ? 1.f : exp2_approx(top - now);
+                ref[lane] = m == -INFINITY ? 0.f : 8.f - m;
+                fac[lane] = c * info.z;
+                grow[lane] = a;
+                grew = a != 1.f;
+                top = now;
+                if (w == 0) sh->top[ob][q0 + lane] = m;
+            }
+            grew = __any_sync(0xffffffffu, grew);
+            __syncwarp();
+            if (grew) {
+#pragma unroll
+                for (int q = 0; q < R; q += 2)
+                    l[q / 2] = __fmul2_rn(l[q / 2], *reinterpret_cast<const float2 *>(grow + q));
+            }
+            uint32_t hi[R / 4], lo[R / 4];
+#pragma unroll
+            for (int q = 0; q < R; q += 4) {
+                const float4 r = *reinterpret_cast<const float4 *>(ref + q);
+                const float4 f = *reinterpret_cast<const float4 *>(fac + q);
+                float2 x = __fadd2_rn(s[q / 2], make_float2(r.x, r.y));
+                float2 y = __fadd2_rn(s[q / 2 + 1], make_float2(r.z, r.w));
+                x.x = exp2_approx(x.x);
+                x.y = exp2_approx(x.y);
+                y.x = exp2_approx(y.x);
+                y.y = exp2_approx(y.y);
+                l[q / 2] = __ffma2_rn(x, make_float2(f.x, f.y), l[q / 2]);
+                l[q / 2 + 1] = __ffma2_rn(y, make_float2(f.z, f.w), l[q / 2 + 1]);
+                uint32_t hx, lx, hy, ly;
+                e4m3_split2(x.x, x.y, hx, lx);
+                e4m3_split2(y.x, y.y, hy, ly);
+                hi[q / 4] = __byte_perm(hx, hy, 0x5410);
+                lo[q / 4] = __byte_perm(lx, ly, 0x5410);
+            }
+            // 16 columns of a key are 16 bytes, keys one after another
+            unsigned char *pk = sP + ob * C::kPBytes + key * 16;
+            if constexpr (NQ == 8) {
+                *reinterpret_cast<uint4 *>(pk) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+            } else {
+                pk += kSplit ? grp * 2048 : 0;
+                *reinterpret_cast<uint4 *>(pk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(pk + (NQ / 16) * 2048) =
+                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (tile.flags & (kSplit ? kFbLast : kFbLastPair)) {    // the group's last of the part
+                float v[R];
+#pragma unroll
+                for (int q = 0; q < R; ++q) v[q] = q & 1 ? l[q / 2].y : l[q / 2].x;
+                const float sum = warp_sums<R>(v, lane);
+                if (lane < R) {
+                    sh->lsum[seg & 3][kSplit ? 0 : grp][w][q0 + lane] = sum;
+                    if (w == 0) sh->ltop[seg & 3][kSplit ? 0 : grp][q0 + lane] = top;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive_warp(&sh->p_full[ob]);
+            if (kSplit && left == 0) break;
+        }
     } else {
-            if constexpr (C::kSplitRegs) regs_increase<C::kRegsOutput>();
-            // ======================================================== output
-            const int w = warp & 3;
-            const uint32_t tlane = (uint32_t)(32 * w) << 16;
-            const int col = C::kM == 64 ? 16 * w + lane : 32 * w + lane;
-            const bool mine = C::kM == 128 || lane < 16;
-            float2 *join = sh->join[w];
-            int n = 0, seg = 0;
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, int phase) {
-                if (ok && !mbar_test(bar, (uint32_t)(phase & 1)))
-                    ok = mbar_wait(bar, (uint32_t)(phase & 1), p.timeout_ns, p.err, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-            };
-            for (; ok && !walk.done(); walk.next(), ++seg) {
-                float2 o[C::kHalves][NQ / 2];
-                float top = -INFINITY;
+        // =========================================================== output
+        const int w = warp & 3;
+        const uint32_t tlane = (uint32_t)(32 * w) << 16;
+        const int col = C::kM == 64 ? 16 * w + lane : 32 * w + lane;
+        const bool mine = C::kM == 128 || lane < 16;
+        float *join = sh->join[w][0], *keep = sh->join[w][1];
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return fb_wait(bar, parity, p, abort_flag);
+        };
+        float2 o[C::kHalves][NQ / 2];
+        float top = -INFINITY;
+        int n0 = 0;                                            // the part's first tile
+        for (int n = 0;; ++n) {
+            const int buf = n % C::kOut;
+            const uint32_t par = (uint32_t)((n / C::kOut) & 1);
+            if (!wait(&sh->p_full[buf], par)) break;
+            const FbTile tile = sh->tile[n % kFbRing];
+            if (tile.flags & kFbFirst) {
+                n0 = n;
+                top = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
                     for (int q = 0; q < NQ / 2; ++q) o[h][q] = make_float2(0.f, 0.f);
-                const int tiles = walk.tiles(), n0 = n;
-                for (int t = 0; ok && t < tiles; ++t, ++n) {
-                    const int buf = n & 1;
-                    wait(&sh->p_full[buf], n >> 1);
-                    if (lane < NQ) {
-                        const float m = sh->top[buf][lane];
-                        const float now = m != m ? m : fmaxf(top, m);
-                        // a tile that the row does not see adds nothing
-                        join[lane] = make_float2(
-                            m == -INFINITY ? 0.f : exp2_approx(m - now - 8.f),
-                            top == now ? 1.f : exp2_approx(top - now));
-                        top = now;
+            }
+            if (lane < NQ) {
+                const float m = sh->top[buf][lane];
+                const float now = m != m ? m : fmaxf(top, m);
+                // a tile that the row does not see adds nothing
+                join[lane] = m == -INFINITY ? 0.f : exp2_approx(m - now - 8.f);
+                keep[lane] = top == now ? 1.f : exp2_approx(top - now);
+                top = now;
+            }
+            __syncwarp();
+            if (!wait(&sh->o_full[buf], par)) break;
+            tc_fence_after();
+            constexpr int kCols = NQ < 16 ? NQ : 16;
+            const float2 piece = make_float2(0.03125f, 0.03125f);
+#pragma unroll
+            for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+                for (int c0 = 0; c0 < NQ; c0 += kCols) {
+                    float xy[2 * kCols];
+                    const uint32_t at = tmem + C::kTmemO + (buf * C::kHalves + h) * C::kN + tlane;
+                    if constexpr (NQ <= 16) {
+                        fb_tmem_ld<2 * kCols>(at, xy);
+                    } else {
+                        tmem_ld16(at + c0, xy);
+                        tmem_ld16(at + NQ + c0, xy + 16);
                     }
-                    __syncwarp();
-                    wait(&sh->o_full[buf], n >> 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    constexpr int kCols = NQ < 16 ? NQ : 16;
-                    const float2 part = make_float2(0.03125f, 0.03125f);
 #pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
+                    for (int q = 0; q < kCols; q += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(join + c0 + q);
+                        const float4 k = *reinterpret_cast<const float4 *>(keep + c0 + q);
+                        const float *x = xy + q, *y = xy + kCols + q;
+                        float2 *d = &o[h][(c0 + q) / 2];
+                        d[0] = __ffma2_rn(__ffma2_rn(make_float2(y[0], y[1]), piece,
+                                                     make_float2(x[0], x[1])),
+                                          make_float2(f.x, f.y),
+                                          __fmul2_rn(d[0], make_float2(k.x, k.y)));
+                        d[1] = __ffma2_rn(__ffma2_rn(make_float2(y[2], y[3]), piece,
+                                                     make_float2(x[2], x[3])),
+                                          make_float2(f.z, f.w),
+                                          __fmul2_rn(d[1], make_float2(k.z, k.w)));
+                    }
+                }
+            if (tile.flags & kFbLast) {
+                const int seg = tile.flags >> kFbSegShift;
+                const FbPart part = sh->part[seg % kFbRing];
+                float sum = 0.f;                               // of row `lane`
+                int out_row = 0;
+                if (lane < part.rows) {
 #pragma unroll
-                        for (int q0 = 0; q0 < NQ; q0 += kCols) {
-                            float xy[2 * kCols];
-                            const uint32_t at =
-                                tmem + C::kTmemO + (buf * C::kHalves + h) * C::kN + tlane;
-                            if constexpr (NQ <= 16) {
-                                fb_tmem_ld<2 * kCols>(at, xy);
-                            } else {
-                                tmem_ld16(at + q0, xy);
-                                tmem_ld16(at + NQ + q0, xy + 16);
-                            }
+                    for (int g = 0; g < (FbShared<NQ>::kRowSplit ? 1 : 2); ++g) {
+                        // the group has a tile of this part
+                        if (!FbShared<NQ>::kRowSplit && n == n0 && (n & 1) != g) continue;
+                        const float lt = sh->ltop[seg & 3][g][lane];
+                        const float *ls = &sh->lsum[seg & 3][g][0][lane];
+                        const float s = (ls[0] + ls[NQ]) + (ls[2 * NQ] + ls[3 * NQ]);
+                        if (lt != -INFINITY) sum = fmaf(s, exp2_approx(lt - top), sum);
+                    }
+                    const int row = part.row0 + lane, i = row / p.group;
+                    out_row = (part.b * p.q_len + i) * p.H_q + part.kvh * p.group +
+                              (row - i * p.group);
+                }
+                if (part.whole) {
+                    const float by = sum != 0.f ? 1.f / sum : 0.f;
+                    __nv_bfloat16 *dst = p.out + col;
 #pragma unroll
-                            for (int q = 0; q < kCols; q += 2) {
-                                const float4 f =
-                                    *reinterpret_cast<const float4 *>(&join[q0 + q]);
-                                float2 &d = o[h][(q0 + q) / 2];
-                                const float2 v = __ffma2_rn(
-                                    make_float2(xy[kCols + q], xy[kCols + q + 1]), part,
-                                    make_float2(xy[q], xy[q + 1]));
-                                d = __ffma2_rn(v, make_float2(f.x, f.z),
-                                               __fmul2_rn(d, make_float2(f.y, f.w)));
-                            }
-                        }
-                    if (t == tiles - 1) {
-                        const FbUnit u = fb_unit(p, walk.w.unit);
-                        float sum = 0.f;               // of row `lane`
-                        int out_row = 0;
-                        if (lane < u.rows) {
+                    for (int q = 0; q < NQ; ++q) {
+                        const float f = __shfl_sync(0xffffffffu, by, q);
+                        const int r = __shfl_sync(0xffffffffu, out_row, q);
+                        if (q < part.rows && mine) {
 #pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                // the group has a tile of this part
-                                if (tiles < 2 && (n0 & 1) != g) continue;
-                                const float lt = sh->ltop[seg & 1][g][lane];
-                                const float *ls = &sh->lsum[seg & 1][g][0][lane];
-                                const float s = (ls[0] + ls[NQ]) + (ls[2 * NQ] + ls[3 * NQ]);
-                                if (lt != -INFINITY) sum = fmaf(s, exp2_approx(lt - top), sum);
-                            }
-                            const int row = u.row0 + lane, i = row / p.group;
-                            out_row = (walk.w.b * p.q_len + i) * p.H_q + u.kvh * p.group +
-                                      (row - i * p.group);
-                        }
-                        if (walk.whole()) {
-                            const float by = sum != 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-                            for (int q = 0; q < NQ; ++q) {
-                                const float f = __shfl_sync(0xffffffffu, by, q);
-                                __nv_bfloat16 *dst =
-                                    p.out +
-                                    (size_t)__shfl_sync(0xffffffffu, out_row, q) * D + col;
-                                if (q < u.rows && mine) {
-#pragma unroll
-                                    for (int h = 0; h < C::kHalves; ++h)
-                                        dst[h * 128] = __float2bfloat16_rn(
-                                            (q & 1 ? o[h][q / 2].y : o[h][q / 2].x) * f);
-                                }
-                            }
-                        } else {
-                            const int slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
-                            float *part_o = p.ws_o + (size_t)slot * NQ * D + col;
-#pragma unroll
-                            for (int q = 0; q < NQ; ++q)
-                                if (q < u.rows && mine) {
-#pragma unroll
-                                    for (int h = 0; h < C::kHalves; ++h)
-                                        part_o[q * D + h * 128] =
-                                            q & 1 ? o[h][q / 2].y : o[h][q / 2].x;
-                                }
-                            if (w == 0 && lane < u.rows)
-                                p.ws_ml[slot * NQ + lane] = make_float2(top, sum);
+                            for (int h = 0; h < C::kHalves; ++h)
+                                dst[(size_t)r * D + h * 128] = __float2bfloat16_rn(
+                                    (q & 1 ? o[h][q / 2].y : o[h][q / 2].x) * f);
                         }
                     }
-                    tc_fence_before();
-                    mbar_arrive_warp(&sh->o_free[buf]);
+                } else {
+                    const int slot = 2 * blockIdx.x + (seg == 0 ? 0 : 1);
+                    float *dst = p.ws_o + (size_t)slot * NQ * D + col;
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+                        if (q < part.rows && mine) {
+#pragma unroll
+                            for (int h = 0; h < C::kHalves; ++h)
+                                dst[q * D + h * 128] = q & 1 ? o[h][q / 2].y : o[h][q / 2].x;
+                        }
+                    if (w == 0 && lane < part.rows)
+                        p.ws_ml[slot * NQ + lane] = make_float2(top, sum);
+                    __threadfence();
                 }
             }
+            tc_fence_before();
+            mbar_arrive_warp(&sh->o_free[buf]);
+            if (tile.left == 0) break;
+        }
     }
 
     // Sequences without a visible key: rows of zeros.
@@ -1023,111 +1238,37 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+    if (p.whole_units || p.join_kernel) return;
+
+    // Units that other CTAs hold parts of: the last one to get here joins them
+    // and leaves the counter (of the unit's first CTA) at zero.
+    if (tid < 2) {
+        const FbCut c = sh->cut[tid];
+        bool last = false;
+        if (c.last >= c.first) {
+            __threadfence();
+            last = atomicAdd(p.ws_count + c.first, 1u) == (unsigned)(c.last - c.first);
+            if (last) p.ws_count[c.first] = 0u;
+            __threadfence();
+        }
+        sh->joins[tid] = last;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int j = 0; j < 2; ++j)
+        if (sh->joins[j]) fb_join<D, NQ>(p, sh->cut[j], smem, 0, 1);
 }
 
-// Joins the partials of the unit that is cut between main CTAs i and i + 1
-// (i = blockIdx.x), if one is.  The CTAs of a unit's cuts share its values;
-// splits are added in order, so a result does not depend on which CTA came
-// first.
-constexpr int kFbJoinThreads = 256;
+// The same as a kernel of its own, which shares out the joining of a unit over
+// the CTAs of its cuts (CTA i: the one between main CTAs i and i + 1).
 template <int D, int NQ>
-__global__ void __launch_bounds__(kFbJoinThreads)
+__global__ void __launch_bounds__(kFbThreads)
 gqa_fp8_block_join_kernel(const GqaFp8BlockParams p) {
-    constexpr int kWarps = kFbJoinThreads / 32;
-    constexpr int kC = D / 4;                  // float4 of a row
-    constexpr int kPer = D == 256 ? 2 : 1;     // of a lane
-    constexpr int kPar = D == 64 ? 2 : 1;      // splits that a warp adds at a time
-    constexpr int kAhead = 4;
-    __shared__ float4 s_o[kWarps][kC * kPar];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    extern __shared__ __align__(16) unsigned char join_smem[];
     pdl_wait_primary();
     const FbCut cut = p.ws_cut[blockIdx.x];
     if (cut.last < cut.first) return;
-    const FbUnit u = fb_unit(p, cut.unit);
-    const int n = cut.last - cut.first + 1;    // splits
-    const int sub = kPar == 2 ? lane >> 4 : 0, c = kPar == 2 ? lane & 15 : lane;
-    auto slot = [&](int k) { return k == 0 ? cut.slot : 2 * (cut.first + k); };
-    for (int q = (int)blockIdx.x - cut.first; q < u.rows; q += n - 1) {
-        // Warp w adds splits w, w + 8, ... (two at once where a row is short),
-        // each lane its columns, relative to the largest reference of them.
-        float top = -INFINITY, sum = 0.f;
-        float4 o[kPer];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = warp * kPar + sub; k0 < n; k0 += kAhead * kWarps * kPar) {
-            float2 ml[kAhead];
-            float4 v[kAhead][kPer];
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int k = k0 + a * kWarps * kPar;
-                ml[a] = make_float2(-INFINITY, 0.f);
-                if (k < n) {
-                    const size_t at = (size_t)slot(k) * NQ + q;
-                    ml[a] = p.ws_ml[at];
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j)
-                        v[a][j] = *reinterpret_cast<const float4 *>(p.ws_o + at * D +
-                                                                    (j * 32 + c) * 4);
-                }
-            }
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                // a split whose keys the row does not see adds nothing
-                if (ml[a].x == -INFINITY) continue;
-                const float now = ml[a].x != ml[a].x ? ml[a].x : fmaxf(top, ml[a].x);
-                const float f = exp2f(ml[a].x - now);
-                const float g = top == now ? 1.f : exp2f(top - now);
-                top = now;
-                sum = fmaf(sum, g, ml[a].y * f);
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    o[j].x = fmaf(o[j].x, g, v[a][j].x * f);
-                    o[j].y = fmaf(o[j].y, g, v[a][j].y * f);
-                    o[j].z = fmaf(o[j].z, g, v[a][j].z * f);
-                    o[j].w = fmaf(o[j].w, g, v[a][j].w * f);
-                }
-            }
-        }
-        // ... and the warps' sums, in order
-        __shared__ float s_top[kWarps * kPar];
-        __shared__ float s_part[kWarps * kPar];
-        __syncthreads();                       // the last row's are read
-        if (c == 0) {
-            s_top[warp * kPar + sub] = top;
-            s_part[warp * kPar + sub] = sum;
-        }
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) s_o[warp][(kPar == 2 ? sub * kC : j * 32) + c] = o[j];
-        __syncthreads();
-        if (tid < kC) {
-            float all = -INFINITY;
-            bool nan = false;
-#pragma unroll
-            for (int k = 0; k < kWarps * kPar; ++k) {
-                nan |= s_top[k] != s_top[k];
-                all = fmaxf(all, s_top[k]);
-            }
-            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-            float total = nan ? NAN : 0.f;
-#pragma unroll
-            for (int k = 0; k < kWarps * kPar; ++k) {
-                const float f = s_top[k] == -INFINITY ? 0.f : exp2f(s_top[k] - all);
-                const float4 x = s_o[k / kPar][(k % kPar) * kC + tid];
-                total = fmaf(f, s_part[k], total);
-                r.x = fmaf(f, x.x, r.x);
-                r.y = fmaf(f, x.y, r.y);
-                r.z = fmaf(f, x.z, r.z);
-                r.w = fmaf(f, x.w, r.w);
-            }
-            const float by = total != 0.f ? 1.f / total : 0.f;
-            const int row = u.row0 + q, i = row / p.group, g = row % p.group;
-            __nv_bfloat162 w[2] = {__floats2bfloat162_rn(r.x * by, r.y * by),
-                                   __floats2bfloat162_rn(r.z * by, r.w * by)};
-            *reinterpret_cast<uint2 *>(p.out + ((size_t)(cut.b * p.q_len + i) * p.H_q +
-                                                u.kvh * p.group + g) * D + tid * 4) =
-                *reinterpret_cast<const uint2 *>(w);
-        }
-    }
+    fb_join<D, NQ>(p, cut, join_smem, (int)blockIdx.x - cut.first, cut.last - cut.first);
 }
 
 // -------------------------------------------------------------- host side
@@ -1139,9 +1280,11 @@ int fp8_block_rows(int rows) {
 
 static int fb_columns(int chunk_rows) { return chunk_rows <= 8 ? 8 : chunk_rows <= 16 ? 16 : 32; }
 
+// The workspace: arrival counters, cuts, partials, their references and sums.
 int64_t fp8_block_workspace_bytes(int num_ctas, int rows, int d) {
     const int64_t nq = fb_columns(fp8_block_rows(rows));
-    return 2ll * num_ctas * nq * (d * 4 + 8) + num_ctas * (int64_t)sizeof(FbCut);
+    return 4 * kFp8BlockMaxCtas + (int64_t)sizeof(FbCut) * kFp8BlockMaxCtas +
+           2ll * num_ctas * nq * (d * 4 + 8);
 }
 
 namespace {
@@ -1167,12 +1310,10 @@ cudaError_t fb_launch(const GqaFp8BlockParams &p, cudaStream_t stream) {
     using C = FbCfg<D, NQ>;
     static PerDeviceFlag configured;
     cudaError_t e = configure_once_per_device(configured, [] {
-        // The shares of a register split must fit in what the kernel is
-        // launched with, or the increase would never be granted.
-        cudaFuncAttributes fa;
-        const cudaError_t r = cudaFuncGetAttributes(&fa, gqa_fp8_block_kernel<D, NQ, G>);
+        const cudaError_t r = cudaFuncSetAttribute(
+            gqa_fp8_block_join_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            kFbThreads * 16 + NQ * kFp8BlockMaxCtas * 4);
         if (r != cudaSuccess) return r;
-        if (C::kSplitRegs && fa.numRegs < 128) return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(gqa_fp8_block_kernel<D, NQ, G>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
@@ -1192,10 +1333,9 @@ cudaError_t fb_launch(const GqaFp8BlockParams &p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, gqa_fp8_block_kernel<D, NQ, G>, tk, tv, p);
-    if (e != cudaSuccess || p.whole_units || p.num_ctas == 1) return e;
+    if (e != cudaSuccess || !p.join_kernel) return e;
     cfg.gridDim = dim3((unsigned)p.num_ctas - 1);
-    cfg.blockDim = dim3(kFbJoinThreads);
-    cfg.dynamicSmemBytes = 0;
+    cfg.dynamicSmemBytes = kFbThreads * 16 + NQ * p.num_ctas * 4;
     return cudaLaunchKernelEx(&cfg, gqa_fp8_block_join_kernel<D, NQ>, p);
 }
 
@@ -1218,13 +1358,19 @@ cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &given, int d, void *wo
     p.chunk_rows = fp8_block_rows(rows);
     p.chunks = (rows + p.chunk_rows - 1) / p.chunk_rows;
     const size_t slots = 2 * (size_t)p.num_ctas * fb_columns(p.chunk_rows);
-    p.ws_o = static_cast<float *>(workspace);
+    p.ws_count = static_cast<unsigned *>(workspace);
+    p.ws_cut = reinterpret_cast<FbCut *>(p.ws_count + kFp8BlockMaxCtas);
+    p.ws_o = reinterpret_cast<float *>(p.ws_cut + kFp8BlockMaxCtas);
     p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + slots * d);
-    p.ws_cut = reinterpret_cast<FbCut *>(p.ws_ml + slots);
     // Where no sequence can be long and there is an SM for every unit, a unit
-    // is not split: that saves the second kernel.
+    // is not split: that saves the plan and the joining.
     p.whole_units = p.max_blocks <= kFbWholeBlocks &&
                     (long long)p.B * p.H_kv * p.chunks <= p.num_ctas;
+    // Partials of a unit, about (CTAs / units + 1) x rows: many of them are
+    // joined by a kernel of their own.
+    p.join_kernel = !p.whole_units && p.num_ctas > 1 &&
+                    (p.num_ctas / ((long long)p.B * p.H_kv * p.chunks) + 1) * p.chunk_rows >
+                        kFbJoinRows;
     p.small_plan = p.B <= 32 &&
                    (double)p.B * p.H_kv * p.chunks * p.max_blocks * (p.num_ctas + 1.0) < 4e9;
     switch (d) {
