@@ -126,9 +126,9 @@ struct FbShared {
     static constexpr int kBars = 4 * kFbMaxStages + 23;
     alignas(16) FbTile tile[kFbRing];
     alignas(16) FbPart part[kFbRing];
-    // Per V slot and block of the tile: K scale x softmax scale (log2 units),
-    // log2 of the V scale, its reciprocal, 0 where the V scale is 0.
-    alignas(16) float4 info[kFbMaxStages][2];
+    // Per tile and block: K scale x softmax scale (log2 units), log2 of the V
+    // scale, its reciprocal, 0 where the V scale is 0.
+    alignas(16) float4 info[kFbRing][2];
     alignas(16) float qsc[kFbRing][NQ];    // power-of-two scale of each query row
     alignas(16) int row_at[kFbRing][NQ];   // its position
     // per softmax group, on even and odd turns: largest scores per warp
@@ -196,13 +196,26 @@ __host__ __device__ constexpr uint32_t fb_idesc(int M, int N, int a_mn, int b_mn
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
+// Issued by the lane whose `lead` is set; the whole warp comes here, so that the
+// descriptors stay in uniform registers (in a branch of one lane each of them is
+// moved there first, 110 cycles an MMA instead of 50).
+__device__ __forceinline__ void umma_f8(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b,
+                                        uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit_by(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(lead)
         : "memory");
 }
 
@@ -231,18 +244,17 @@ __device__ __forceinline__ bool fb_wait(uint64_t *bar, uint32_t parity,
     return __all_sync(0xffffffffu, fb_wait_slow(bar, parity, p.timeout_ns, p.err, abort));
 }
 
-// The same by testing the barrier over and over: for the threads that issue
-// the products, which everything else waits on (a suspended wait wakes up some
-// 200 cycles late).
+// The same for the warps that issue the products, which everything else waits
+// on: they never sleep.
 __device__ __noinline__ bool fb_poll_slow(uint64_t *bar, uint32_t parity,
                                           unsigned long long timeout_ns, unsigned *err,
                                           volatile int *abort) {
     unsigned long long t0 = 0;
     for (uint32_t it = 0;; ++it) {
-        if (mbar_test(bar, parity)) return true;
-        if ((it & 15u) == 15u && *abort) return false;
+        if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+        if ((it & 15u) == 15u && __any_sync(0xffffffffu, *abort)) return false;
         if ((it & 1023u) == 1023u) {
-            const unsigned long long now = global_timer_ns();
+            const unsigned long long now = __shfl_sync(0xffffffffu, global_timer_ns(), 0);
             if (t0 == 0) {
                 t0 = now;
             } else if (now - t0 > timeout_ns) {
@@ -698,13 +710,6 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                     ok = tile < C::kKStages || mbar_test(&sh->k_empty[ks], k_par) ||
                          fb_wait_slow(&sh->k_empty[ks], k_par, p.timeout_ns, p.err, abort_flag);
                     if (ok) {
-                        const int at = base0 + j;
-                        sh->tile[tile % kFbRing] =
-                            FbTile{{pos0, pos1},
-                                   (two ? kFbTwo : 0) | (at == 0 ? kFbFirst : 0) | (at + 2 >= len ? kFbLast : 0) |
-                                       (at + 4 >= len ? kFbLastPair : 0) | seg << kFbSegShift,
-                                   left};
-                        mbar_arrive_expect_tx(&sh->k_full[ks], bytes);
 #pragma unroll
                         for (int x = 0; x < C::kBoxes; ++x) {
                             unsigned char *dst = sK + ks * C::kSlot + x * C::kBoxBytes;
@@ -713,19 +718,24 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 tma_load_2d(dst + kBlockSize * C::kRowBytes, &tm_k,
                                             x * C::kRowBytes, row1, &sh->k_full[ks], pol);
                         }
-                        n_k = tile + 1;
-                        ok = tile < C::kVStages || mbar_test(&sh->v_empty[vs], v_par) ||
-                             fb_wait_slow(&sh->v_empty[vs], v_par, p.timeout_ns, p.err,
-                                          abort_flag);
+                        const int at = base0 + j;
+                        sh->tile[tile % kFbRing] =
+                            FbTile{{pos0, pos1},
+                                   (two ? kFbTwo : 0) | (at == 0 ? kFbFirst : 0) |
+                                       (at + 2 >= len ? kFbLast : 0) |
+                                       (at + 4 >= len ? kFbLastPair : 0) | seg << kFbSegShift,
+                                   left};
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
+                // The scales may arrive after the copies set out: the arrival
+                // that lets others see the tile comes behind them.
                 if (lane == j || lane == j + 1) {
                     // A scale of 0 makes the values 0, not the weights: they
                     // enter the sum through any other scale.
                     const float vse = my_vs == 0.f ? 5.421010862427522e-20f /* 2^-64 */ : my_vs;
-                    sh->info[vs][lane - j] =
+                    sh->info[tile % kFbRing][lane - j] =
                         my_block && lane < count
                             ? make_float4(my_ks * p.scale_log2, log2f(vse), 1.f / vse,
                                           my_vs == 0.f ? 0.f : 1.f)
@@ -733,17 +743,25 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&sh->v_full[vs], bytes);
+                    mbar_arrive_expect_tx(&sh->k_full[ks], bytes);
+                    n_k = tile + 1;
+                    ok = tile < C::kVStages || mbar_test(&sh->v_empty[vs], v_par) ||
+                         fb_wait_slow(&sh->v_empty[vs], v_par, p.timeout_ns, p.err, abort_flag);
+                    if (ok) {
+                        mbar_arrive_expect_tx(&sh->v_full[vs], bytes);
 #pragma unroll
-                    for (int x = 0; x < C::kBoxes; ++x) {
-                        unsigned char *dst = sV + vs * C::kSlot + x * C::kBoxBytes;
-                        tma_load_2d(dst, &tm_v, x * C::kRowBytes, row0, &sh->v_full[vs], pol);
-                        if (two)
-                            tma_load_2d(dst + kBlockSize * C::kRowBytes, &tm_v, x * C::kRowBytes,
-                                        row1, &sh->v_full[vs], pol);
+                        for (int x = 0; x < C::kBoxes; ++x) {
+                            unsigned char *dst = sV + vs * C::kSlot + x * C::kBoxBytes;
+                            tma_load_2d(dst, &tm_v, x * C::kRowBytes, row0, &sh->v_full[vs], pol);
+                            if (two)
+                                tma_load_2d(dst + kBlockSize * C::kRowBytes, &tm_v,
+                                            x * C::kRowBytes, row1, &sh->v_full[vs], pol);
+                        }
+                        n_v = tile + 1;
                     }
-                    n_v = tile + 1;
                 }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
                 if (++ks == C::kKStages) {
                     ks = 0;
                     k_par ^= 1u;
@@ -776,91 +794,91 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
         __syncwarp();
     } else if (warp == 1) {
         // ===================================================== S^T = K Q^T
-        if (lane == 0) {
-            constexpr uint32_t idesc = fb_idesc(128, C::kN, 0, 0);
-            constexpr int kLayout = C::kRowBytes == 128 ? 2 : 4;
-            constexpr int kSteps = C::kRowBytes / 32;
-            const uint64_t dk = fb_desc(smem_u32(sK), 16, C::kRowBytes * 8, kLayout);
-            const uint64_t dq = fb_desc(smem_u32(sQ), 16, C::kRowBytes * 8, kLayout);
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                return mbar_test(bar, parity) ||
-                       fb_poll_slow(bar, parity, p.timeout_ns, p.err, abort_flag);
-            };
-            int ks = 0;
-            uint32_t k_par = 0;
-            for (int n = 0;; ++n) {
-                if (n >= 2 && !wait(&sh->s_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) break;
-                if (!wait(&sh->k_full[ks], k_par)) break;
-                const FbTile at = sh->tile[n % kFbRing];
-                const int seg = at.flags >> kFbSegShift;
-                if ((at.flags & kFbFirst) &&
-                    !wait(&sh->q_full[seg & 1], (uint32_t)((seg >> 1) & 1)))
-                    break;
-                tc_fence_after();
-#pragma unroll
-                for (int s = 0; s < C::kBoxes * kSteps; ++s) {
-                    const int x = s / kSteps, o = (s % kSteps) * 32;
-                    // addresses count in 16 bytes
-                    umma_f8(tmem + C::kTmemS + (n & 1) * C::kN,
-                            dk + ((ks * C::kSlot + x * C::kBoxBytes + o) >> 4),
-                            dq + (((seg & 1) * C::kQBytes + x * C::kN * C::kRowBytes + o) >> 4),
-                            idesc, s != 0);
-                }
-                umma_commit(&sh->s_full[n & 1]);
-                // what this thread has seen (the rows' scales), the softmax may too
-                mbar_arrive(&sh->s_full[n & 1]);
-                umma_commit(&sh->k_empty[ks]);
-                if (at.flags & kFbLast) umma_commit(&sh->q_empty[seg & 1]);
-                if (at.left == 0) break;
-                if (++ks == C::kKStages) {
-                    ks = 0;
-                    k_par ^= 1u;
-                }
+        constexpr uint32_t idesc = fb_idesc(128, C::kN, 0, 0);
+        constexpr int kLayout = C::kRowBytes == 128 ? 2 : 4;
+        constexpr int kSteps = C::kRowBytes / 32;
+        const uint64_t dk = fb_desc(smem_u32(sK), 16, C::kRowBytes * 8, kLayout);
+        const uint64_t dq = fb_desc(smem_u32(sQ), 16, C::kRowBytes * 8, kLayout);
+        const uint32_t lead = lane == 0;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_test(bar, parity)) ||
+                   fb_poll_slow(bar, parity, p.timeout_ns, p.err, abort_flag);
+        };
+        int ks = 0, seg = -1;
+        uint32_t k_par = 0;
+        for (int n = 0;; ++n) {
+            if (n >= 2 && !wait(&sh->s_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) break;
+            if (!wait(&sh->k_full[ks], k_par)) break;
+            const FbTile at = sh->tile[n % kFbRing];
+            if (__any_sync(0xffffffffu, at.flags & kFbFirst)) {
+                ++seg;
+                if (!wait(&sh->q_full[seg & 1], (uint32_t)((seg >> 1) & 1))) break;
             }
-            umma_commit(&sh->mma_final);
+            tc_fence_after();
+            const uint32_t d = tmem + C::kTmemS + (n & 1) * C::kN;
+            const uint64_t a0 = dk + ((ks * C::kSlot) >> 4);   // addresses count in 16 bytes
+            const uint64_t b0 = dq + (((seg & 1) * C::kQBytes) >> 4);
+#pragma unroll
+            for (int s = 0; s < C::kBoxes * kSteps; ++s) {
+                const int x = s / kSteps, o = (s % kSteps) * 32;
+                umma_f8(lead, d, a0 + ((x * C::kBoxBytes + o) >> 4),
+                        b0 + ((x * C::kN * C::kRowBytes + o) >> 4), idesc, s != 0);
+            }
+            umma_commit_by(lead, &sh->s_full[n & 1]);
+            // what this thread has seen (tile, scales), the softmax may too
+            if (lead) mbar_arrive(&sh->s_full[n & 1]);
+            umma_commit_by(lead, &sh->k_empty[ks]);
+            if (__any_sync(0xffffffffu, at.flags & kFbLast))
+                umma_commit_by(lead, &sh->q_empty[seg & 1]);
+            if (__any_sync(0xffffffffu, at.left == 0)) break;
+            if (++ks == C::kKStages) {
+                ks = 0;
+                k_par ^= 1u;
+            }
         }
+        umma_commit_by(lead, &sh->mma_final);
         __syncwarp();
     } else if (warp == 2) {
         // ====================================================== O^T = V^T P
-        if (lane == 0) {
-            constexpr uint32_t idesc = fb_idesc(C::kM, C::kN, 1, 1);
-            constexpr int kLayout = C::kRowBytes == 128 ? 2 : 4;
-            const uint64_t dv = fb_desc(smem_u32(sV), 16, C::kRowBytes * 8, kLayout);
-            const uint64_t dp = fb_desc(smem_u32(sP), 128, 2048, 0);
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                return mbar_test(bar, parity) ||
-                       fb_poll_slow(bar, parity, p.timeout_ns, p.err, abort_flag);
-            };
-            int vs = 0;
-            uint32_t v_par = 0;
-            for (int n = 0;; ++n) {
-                if (!wait(&sh->v_full[vs], v_par)) break;
-                const int buf = n % C::kOut;
-                const uint32_t par = (uint32_t)((n / C::kOut) & 1);
-                if (n >= C::kOut && !wait(&sh->o_free[buf], par ^ 1u)) break;
-                if (!wait(&sh->p_full[buf], par)) break;
-                tc_fence_after();
+        constexpr uint32_t idesc = fb_idesc(C::kM, C::kN, 1, 1);
+        constexpr int kLayout = C::kRowBytes == 128 ? 2 : 4;
+        const uint64_t dv = fb_desc(smem_u32(sV), 16, C::kRowBytes * 8, kLayout);
+        const uint64_t dp = fb_desc(smem_u32(sP), 128, 2048, 0);
+        const uint32_t lead = lane == 0;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_test(bar, parity)) ||
+                   fb_poll_slow(bar, parity, p.timeout_ns, p.err, abort_flag);
+        };
+        int vs = 0;
+        uint32_t v_par = 0;
+        for (int n = 0;; ++n) {
+            const int buf = n % C::kOut;
+            const uint32_t par = (uint32_t)((n / C::kOut) & 1);
+            if (!wait(&sh->v_full[vs], v_par)) break;
+            if (n >= C::kOut && !wait(&sh->o_free[buf], par ^ 1u)) break;
+            if (!wait(&sh->p_full[buf], par)) break;
+            tc_fence_after();
+            const uint32_t d = tmem + C::kTmemO + buf * (C::kHalves * C::kN);
+            const uint64_t a0 = dv + ((vs * C::kSlot) >> 4);
+            const uint64_t b0 = dp + ((buf * C::kPBytes) >> 4);
 #pragma unroll
-                for (int h = 0; h < C::kHalves; ++h)
+            for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-                    for (int s = 0; s < kFbTile / 32; ++s)
-                        umma_f8(tmem + C::kTmemO + (buf * C::kHalves + h) * C::kN,
-                                dv + ((vs * C::kSlot + h * C::kBoxBytes + s * 32 * C::kRowBytes) >>
-                                      4),
-                                dp + ((buf * C::kPBytes + s * 512) >> 4), idesc, s != 0);
-                const int left = sh->tile[n % kFbRing].left;
-                umma_commit(&sh->o_full[buf]);
-                umma_commit(&sh->v_empty[vs]);
-                if (left == 0) break;
-                if (++vs == C::kVStages) {
-                    vs = 0;
-                    v_par ^= 1u;
-                }
+                for (int s = 0; s < kFbTile / 32; ++s)
+                    umma_f8(lead, d + h * C::kN,
+                            a0 + ((h * C::kBoxBytes + s * 32 * C::kRowBytes) >> 4),
+                            b0 + ((s * 512) >> 4), idesc, s != 0);
+            umma_commit_by(lead, &sh->o_full[buf]);
+            umma_commit_by(lead, &sh->v_empty[vs]);
+            if (__any_sync(0xffffffffu, sh->tile[n % kFbRing].left == 0)) break;
+            if (++vs == C::kVStages) {
+                vs = 0;
+                v_par ^= 1u;
             }
-            umma_commit(&sh->mma_final);
-            // Both issuers' products are done before tensor memory is freed.
-            fb_wait_slow(&sh->mma_final, 0, p.timeout_ns, p.err, abort_flag + 1);
         }
+        umma_commit_by(lead, &sh->mma_final);
+        // Both issuers' products are done before tensor memory is freed.
+        fb_wait_slow(&sh->mma_final, 0, p.timeout_ns, p.err, abort_flag + 1);
         __syncwarp();
     } else if (warp == 3) {
         // ====================================================== next queries
@@ -931,15 +949,14 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (left <= 1) break;
                 if (left == 2) {
                     const int o = n - 1;
-                    if (!wait(&sh->v_full[o % C::kVStages], (uint32_t)((o / C::kVStages) & 1)))
-                        break;
+                    if (!wait(&sh->s_full[o & 1], (uint32_t)((o >> 1) & 1))) break;
                     if (sh->tile[o % kFbRing].left == 0) break;
                 }
             }
-            const int buf = n & 1, vs = n % C::kVStages, ob = n % C::kOut;
-            if (!wait(&sh->v_full[vs], (uint32_t)((n / C::kVStages) & 1))) break;
+            const int buf = n & 1, ob = n % C::kOut;
+            if (!wait(&sh->s_full[buf], (uint32_t)((n >> 1) & 1))) break;
             const FbTile tile = sh->tile[n % kFbRing];
-            const float4 info = sh->info[vs][half];
+            const float4 info = sh->info[n % kFbRing][half];
             left = tile.left;
             if ((tile.flags >> kFbSegShift) != seg) {
                 seg = tile.flags >> kFbSegShift;
@@ -963,6 +980,8 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // Rows that no query sees may hold NaN codes: they are zeroed,
                 // since 0 x NaN would reach every row's sum.  So are those whose
                 // scale is 0.  (Row split: either group zeroes half of a row.)
+                const int vs = n % C::kVStages;
+                if (!wait(&sh->v_full[vs], (uint32_t)((n / C::kVStages) & 1))) break;
                 if (!(there && pos < T && info.w != 0.f && (early || pos > T - L - window))) {
                     constexpr int kZero = C::kRowBytes / 16 / (kSplit ? 2 : 1);
                     uint4 *v = reinterpret_cast<uint4 *>(sV + vs * C::kSlot +
@@ -975,7 +994,6 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                             v[x * (C::kBoxBytes / 16) + c] = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
-            if (!wait(&sh->s_full[buf], (uint32_t)((n >> 1) & 1))) break;
             tc_fence_after();
             float2 s[R / 2];
             {
@@ -1018,6 +1036,9 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                     if ((unsigned)(at.w - pos) >= span) s[q / 2 + 1].y = -INFINITY;
                 }
             }
+            // The P buffer, and what goes with it, is free again (long ago, as a
+            // rule: tested here, where the scores' arithmetic hides it).
+            if (n >= C::kOut && !wait(&sh->o_free[ob], (uint32_t)((n / C::kOut - 1) & 1))) break;
             // largest of the tile, per row (every lane has it: one writes)
             {
                 float m[R];
@@ -1035,8 +1056,6 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             mbar_arrive_warp(&sh->g_sync[grp]);
             if (!wait(&sh->g_sync[grp], (uint32_t)(turns & 1))) break;
-            // the P buffer, and what goes with it, is free again
-            if (n >= C::kOut && !wait(&sh->o_free[ob], (uint32_t)((n / C::kOut - 1) & 1))) break;
             bool grew = false;
             if (lane < R) {
                 const float(*wm)[R] = sh->wmax[grp][turns & 1];
@@ -1215,7 +1234,6 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     if (w == 0 && lane < part.rows)
                         p.ws_ml[slot * NQ + lane] = make_float2(top, sum);
-                    __threadfence();
                 }
             }
             tc_fence_before();
