@@ -7,7 +7,6 @@ the current CUDA stream, and raises AttnError on a failing status.  There is
 no fallback: if the library is missing, ``load()`` raises.
 """
 import ctypes
-import functools
 import os
 
 import torch
@@ -424,32 +423,20 @@ def _at(t, name, dtype, dev, shape=None, dense=True):
     return t.data_ptr()
 
 
-def _device_of(t, name):
+def _place(t, name, stream):
+    """(device, stream handle, context or None) of a call whose first tensor is t:
+    the given stream, else the device's current one.  The context makes the
+    device current, and the stream too if given (what the call allocates is its)."""
     dev = t.get_device() if isinstance(t, torch.Tensor) else -1
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
-
-
-def _on_device(call):
-    """Runs `call(dev, stream handle, ...)` on the device of its first argument
-    and the given stream (else that device's current one)."""
-    @functools.wraps(call)
-    def run(first, *args, stream=None, **kwargs):
-        dev = _device_of(first, call.__code__.co_varnames[2])
-        if stream is None:
-            handle = torch._C._cuda_getCurrentRawStream(dev)
-        elif stream.device_index == dev:
-            handle = stream.cuda_stream
-            with torch.cuda.stream(stream):          # what the call allocates is the stream's
-                return call(dev, handle, first, *args, **kwargs)
-        else:
-            raise ValueError("the stream belongs to another device than the tensors")
-        if torch._C._cuda_getDevice() != dev:
-            with torch.cuda.device(dev):
-                return call(dev, handle, first, *args, **kwargs)
-        return call(dev, handle, first, *args, **kwargs)
-    return run
+    if stream is None:
+        if torch._C._cuda_getDevice() == dev:
+            return dev, torch._C._cuda_getCurrentRawStream(dev), None
+        return dev, torch._C._cuda_getCurrentRawStream(dev), torch.cuda.device(dev)
+    if stream.device_index != dev:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return dev, stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _block_cache(dev, k_cache, v_cache, k_scale, v_scale):
@@ -503,7 +490,6 @@ def _rows_of(dev, t, name, dtype, tail):
     return at, row[0] if t.shape[0] > 1 else tail[0] * tail[1]
 
 
-@_on_device
 def _append_fp8_block(dev, stream, k_new, v_new, k_cache, v_cache, k_scale, v_scale, positions,
                       block_table, offsets, window, sink_tokens, ring_blocks, global_pos):
     (kc, vc, ks, vs), nblk, H_kv, d = _block_cache(dev, k_cache, v_cache, k_scale, v_scale)
@@ -536,11 +522,17 @@ def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, positi
     b's.  A block whose first row is written takes the scale its rows ask for;
     a block begun earlier keeps its scale or grows it, its codes rounded to the
     new one."""
-    _append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, positions, block_table,
-                      offsets, window, sink_tokens, ring_blocks, global_pos, stream=stream)
+    dev, handle, where = _place(k_new, "k_new", stream)
+    if where is None:
+        return _append_fp8_block(dev, handle, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                 positions, block_table, offsets, window, sink_tokens, ring_blocks,
+                                 global_pos)
+    with where:
+        return _append_fp8_block(dev, handle, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                 positions, block_table, offsets, window, sink_tokens, ring_blocks,
+                                 global_pos)
 
 
-@_on_device
 def _read_fp8_block(dev, stream, k_cache, v_cache, k_scale, v_scale, positions, block_table,
                     n, offsets, dtype, out, window, sink_tokens, ring_blocks, global_pos):
     (kc, vc, ks, vs), nblk, H_kv, d = _block_cache(dev, k_cache, v_cache, k_scale, v_scale)
@@ -574,9 +566,15 @@ def kv_read_fp8_block(k_cache, v_cache, k_scale, v_scale, positions, block_table
     positions[b] + t of sequence b; without offsets row b is positions[b].
     `out`: a pair to write into, whose rows behind offsets[B] are left as they
     were; in new tensors they are zeros."""
-    return _read_fp8_block(k_cache, v_cache, k_scale, v_scale, positions, block_table,
-                           int(n_tokens), offsets, dtype, out, window, sink_tokens, ring_blocks,
-                           global_pos, stream=stream)
+    dev, handle, where = _place(k_cache, "k_cache", stream)
+    if where is None:
+        return _read_fp8_block(dev, handle, k_cache, v_cache, k_scale, v_scale, positions,
+                               block_table, int(n_tokens), offsets, dtype, out, window,
+                               sink_tokens, ring_blocks, global_pos)
+    with where:
+        return _read_fp8_block(dev, handle, k_cache, v_cache, k_scale, v_scale, positions,
+                               block_table, int(n_tokens), offsets, dtype, out, window,
+                               sink_tokens, ring_blocks, global_pos)
 
 
 def _block_queries(q):
@@ -612,7 +610,6 @@ def fp8_block_workspace(q, k_cache):
         return torch.zeros(n, dtype=torch.uint8, device=q.device)
 
 
-@_on_device
 def _decode_fp8_block(dev, stream, q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table,
                       scale, window, sink_tokens, ring_blocks, out, global_pos, workspace):
     (kc, vc, ks, vs), nblk, H_kv, d = _block_cache(dev, k_cache, v_cache, k_scale, v_scale)
@@ -629,7 +626,7 @@ def _decode_fp8_block(dev, stream, q, k_cache, v_cache, k_scale, v_scale, seq_le
         workspace = fp8_block_workspace(q, k_cache)
     wp = _at(workspace, "workspace", torch.uint8, dev)
     if out is None:
-        out = torch.empty(shape, dtype=bf, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = out.data_ptr()
     else:
         op = _at(out, "out", bf, dev, shape)
@@ -651,9 +648,15 @@ def decode_gqa_fp8_block(q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_
     positions or global set (q_len 1 only).  Rows that see nothing are zero.
     `workspace`: from fp8_block_workspace, not shared with a call that may run
     at the same time; without it each call takes a new one."""
-    return _decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table,
-                             float(scale), window, sink_tokens, ring_blocks, out, global_pos,
-                             workspace, stream=stream)
+    dev, handle, where = _place(q, "q", stream)
+    if where is None:
+        return _decode_fp8_block(dev, handle, q, k_cache, v_cache, k_scale, v_scale, seq_lens,
+                                 block_table, scale, window, sink_tokens, ring_blocks, out,
+                                 global_pos, workspace)
+    with where:
+        return _decode_fp8_block(dev, handle, q, k_cache, v_cache, k_scale, v_scale, seq_lens,
+                                 block_table, scale, window, sink_tokens, ring_blocks, out,
+                                 global_pos, workspace)
 
 
 def plan(seq_lens, units_per_seq, window, max_blocks, num_ctas, stream=None):
