@@ -607,7 +607,7 @@ def fp8_block_workspace(q, k_cache):
         n = load().attn_decode_gqa_fp8_block_workspace(B, L, H_q, k_cache.shape[1], d)
         if n < 0:
             raise AttnError(n, "attn_decode_gqa_fp8_block_workspace")
-        return torch.zeros(n, dtype=torch.uint8, device=q.device)
+        return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
 def _decode_fp8_block(dev, stream, q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_table,

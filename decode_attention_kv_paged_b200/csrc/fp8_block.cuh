@@ -37,11 +37,11 @@ cudaError_t launch_kv_append_fp8_block(const KvAppendBlockParams &p, int d, bool
 cudaError_t launch_kv_read_fp8_block(const KvReadBlockParams &p, int d, bool bf16,
                                      cudaStream_t stream);
 
-// Most CTAs of a decode launch: its workspace begins with a counter for each.
+// Most CTAs of a decode launch: its workspace begins with a cut for each.
 constexpr int kFp8BlockMaxCtas = 512;
 
-// A unit that several CTAs hold parts of: those CTAs, the first one's partial,
-// sequence and unit; last < first where there is none.
+// A unit cut at the end of a CTA's range: the CTAs that hold it, the first
+// one's partial, sequence and unit; last < first where nothing is cut.
 struct FbCut {
     int first, last, slot, b, unit;
 };
@@ -65,9 +65,7 @@ struct GqaFp8BlockParams {
     int chunk_rows, chunks;
     float *ws_o;
     float2 *ws_ml;
-    unsigned *ws_count;           // arrivals at a cut unit; zero between launches
-    FbCut *ws_cut;                // for the join kernel: the unit cut at each CTA's end
-    bool join_kernel;             // cut units are joined by a second kernel
+    FbCut *ws_cut;                // the unit cut at each CTA's end
     bool whole_units;             // one CTA per unit, nothing split
     bool small_plan;              // few sequences, a list that 32 bits count
 };

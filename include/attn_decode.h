@@ -496,9 +496,9 @@ int kv_read_fp8_block(const void *k_cache, const void *v_cache, const float *k_s
  * be anything, NaN included; a NaN in a row that one query of the sequence
  * sees may reach that sequence's other queries.
  * workspace: device memory of at least attn_decode_gqa_fp8_block_workspace
- * bytes, 256-byte aligned, zeroed before its first use (each call leaves its
- * counters at zero), which nothing else uses until the call's work is done (a
- * captured graph keeps its own).  ATTN_ERR_ARG if it is too small.  Allocates nothing.  Other errors as
+ * bytes, 256-byte aligned, which nothing else uses until the call's work is
+ * done (a captured graph keeps its own); its contents need no preparation.
+ * ATTN_ERR_ARG if it is too small.  Allocates nothing.  Other errors as
  * attn_decode_gqa_ext.
  */
 int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cache,
