@@ -631,8 +631,8 @@ def _decode_fp8_block(dev, stream, q, k_cache, v_cache, k_scale, v_scale, seq_le
     else:
         op = _at(out, "out", bf, dev, shape)
     rc = load().attn_decode_gqa_fp8_block(qp, q_stride, kc, vc, ks, vs, lens, tab, op, B, L, H_q,
-                                          H_kv, d, scale, vis, wp, workspace.numel(), stream,
-                                          block_table.shape[1], nblk)
+                                          H_kv, d, float(scale), vis, wp, workspace.numel(),
+                                          stream, block_table.shape[1], nblk)
     if rc:
         _check(rc, "attn_decode_gqa_fp8_block")
     return out

@@ -300,10 +300,13 @@ DECODES = [
 
 
 def _decode_case(lib, rng, H_q, H_kv, d, lens, q_len, window, sink, ring=0, global_pos=None,
-                 lo=-8, hi=-4, table=None, tweak=None, scale=None, ctas=0, **call):
+                 lo=-8, hi=-4, table=None, tweak=None, scale=None, ctas=0, wide=0, **call):
     B = len(lens)
     if table is None:
         table, total = _table(rng, [-(-t // BLOCK_SIZE) for t in lens])
+        if wide > table.shape[1]:              # room for sequences that are longer yet
+            more = np.full((B, wide - table.shape[1]), -1, dtype=np.int32)
+            table = np.concatenate([table, more], axis=1)
     else:
         total = int(table.max()) + 1
     cache = _Cache(rng, total, H_kv, d, lo, hi)
@@ -343,6 +346,36 @@ def test_decode_matches_oracle(lib, case, ctas):
     _check(got, cache, inputs, lens, window, sink)
     none = [[max(t - q_len + i + 1, 0) == 0 for i in range(q_len)] for t in lens]
     assert (got[torch.tensor(none, device=DEV)] == 0).all()
+
+
+@pytest.mark.parametrize("ctas", [0, 1, 3], ids=["all_sms", "1_cta", "3_ctas"])
+@pytest.mark.parametrize("case", DECODES, ids=[f"q{c[0]}_kv{c[1]}_d{c[2]}_L{c[4]}_w{c[5]}"
+                                               for c in DECODES])
+def test_decode_split_over_ctas(lib, case, ctas):
+    """A table wide enough for long sequences: the same units, cut anywhere."""
+    H_q, H_kv, d, lens, q_len, window, sink = case
+    rng = np.random.default_rng(60 + H_q + d)
+    got, cache, inputs = _decode_case(lib, rng, *case, ctas=ctas, wide=100)
+    _check(got, cache, inputs, lens, window, sink)
+
+
+@pytest.mark.parametrize("q_len,window", [(1, 0), (3, 100)])
+def test_decode_many_sequences(lib, q_len, window):
+    """More sequences than one warp plans for, some of them empty."""
+    rng = np.random.default_rng(61)
+    lens = [(37 * i * i) % 700 for i in range(45)]
+    for wide in (0, 100):
+        got, cache, inputs = _decode_case(lib, rng, 4, 2, 64, lens, q_len, window, 0, wide=wide)
+        _check(got, cache, inputs, lens, window, 0)
+
+
+def test_decode_many_short_units_of_a_cta(lib):
+    """Units of one block each, several to a CTA: every ring turns over."""
+    rng = np.random.default_rng(62)
+    lens = [1 + (11 * i) % 64 for i in range(30)]
+    for H_q, H_kv, d in ((32, 32, 64), (32, 8, 256), (64, 2, 128)):
+        got, cache, inputs = _decode_case(lib, rng, H_q, H_kv, d, lens, 1, 0, 0, wide=100, ctas=5)
+        _check(got, cache, inputs, lens, 0, 0)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
@@ -439,12 +472,13 @@ def test_decode_ring_table(lib, sink, q_len):
     _check(got, cache, inputs, lens, window, sink, ring=ring)
 
 
-@pytest.mark.parametrize("d", [64, 256])
-def test_decode_global_set(lib, d):
+@pytest.mark.parametrize("H_q,d,wide", [(8, 64, 0), (8, 256, 50), (64, 128, 50)])
+def test_decode_global_set(lib, H_q, d, wide):
     rng = np.random.default_rng(37)
     lens, window = [900, 300, 640], 128
     gp = np.array([[0, 5, 200, 201], [299, -1, -1, -1], [64, 127, 639, -1]], dtype=np.int32)
-    got, cache, inputs = _decode_case(lib, rng, 8, 2, d, lens, 1, window, 0, global_pos=gp)
+    got, cache, inputs = _decode_case(lib, rng, H_q, 2, d, lens, 1, window, 0, global_pos=gp,
+                                      wide=wide)
     _check(got, cache, inputs, lens, window, 0, global_pos=gp)
 
 
