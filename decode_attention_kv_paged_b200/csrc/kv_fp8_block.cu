@@ -4,7 +4,9 @@
 // block's scale is the power of two that its largest new value asks for, so
 // one CTA sees every new row of the block, holds them in registers between
 // finding the maximum and writing the codes, and reads each input once.
-// Read-back: one CTA per (block, up to 8 heads, K or V), 16-byte stores.
+// Read-back: one CTA per (block, up to 8 heads, K or V), 16-byte stores; 128 MiB
+// of codes to bf16 take 69 us, 0.88 of the copy rate (152 us with one head a CTA
+// and a thread's 16 values in two stores).
 // Both are bound by memory; what is left beside that is the chain of dependent
 // loads that finds a CTA its rows (offsets and positions, block table, data).
 #include <cuda_fp8.h>
@@ -13,7 +15,7 @@
 
 namespace attn {
 
-constexpr int kRunThreads = 256;
+constexpr int kRunThreads = 256;      // of the read-back
 
 // Part of a run that falls into one block.
 struct BlockRun {
@@ -181,17 +183,19 @@ template <> struct CodesOf<4> { using type = uint32_t; };
 template <> struct CodesOf<8> { using type = uint2; };
 template <> struct CodesOf<16> { using type = uint4; };
 
-// Thread t takes kE values of input rows t / (D / kE) + kRows k: 8 in bf16, 16
-// in fp32 (4 values, a 16-byte load and a 4-byte store at a time, took 124 us
-// for 256 MiB of fp32 rows, 16 take 110 us).
+// D threads; thread t takes 16 values of input rows t / (D / 16) + 16 k.  Few
+// threads with much in flight each: what bounds the kernel beside HBM is the
+// time of a CTA (three loads that wait for one another), so the bytes that all
+// resident CTAs hold together count.  Measured: 256 MiB of fp32 rows of d = 64
+// 109 us (0.94 of the copy rate; 124 with 256 threads of 4 values), 107 MB of
+// bf16 rows of d = 64 32 us (0.76; 47 with 256 threads of 8 values).
 template <typename T, int D>
-__global__ void __launch_bounds__(kRunThreads)
+__global__ void __launch_bounds__(D, (sizeof(T) == 2 ? 1024 : 640) / D)
 kv_append_fp8_block_kernel(const KvAppendBlockParams p) {
-    constexpr int kC = sizeof(T) == 4 ? 4 : 1;             // 16-byte chunks of a thread's row
-    constexpr int kE = In<T>::kE * kC, kTpr = D / kE, kRows = kRunThreads / kTpr;
-    constexpr int kPasses = kBlockSize / kRows;
+    constexpr int kE = 16, kC = sizeof(T);                 // values, 16-byte chunks of them
+    constexpr int kTpr = D / kE, kRows = D / kTpr, kPasses = kBlockSize / kRows;
     using Codes = typename CodesOf<kE>::type;
-    __shared__ float s_max[kRunThreads / 32];
+    __shared__ float s_max[D / 32];
     const int tid = threadIdx.x, h = blockIdx.y;
     const bool is_v = blockIdx.z != 0;
     pdl_wait_primary();
@@ -237,7 +241,7 @@ kv_append_fp8_block_kernel(const KvAppendBlockParams p) {
     if ((tid & 31) == 0) s_max[tid >> 5] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kRunThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+    for (int w = 0; w < D / 32; ++w) amax = fmaxf(amax, s_max[w]);
 
     const float old = held > 0.f ? held : 0.f;
     const float s = fmaxf(old, block_scale(amax));
@@ -346,13 +350,13 @@ unsigned run_columns(const KvRunParams &r, bool rest) {
 // Programmatic launch: the kernels wait for what came before themselves, and
 // what comes next may be set up while they run.
 template <typename K, typename... A>
-cudaError_t launch_run(K kernel, dim3 grid, cudaStream_t stream, A... args) {
+cudaError_t launch_run(K kernel, dim3 grid, int threads, cudaStream_t stream, A... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kRunThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -363,9 +367,9 @@ template <typename T>
 cudaError_t append_d(const KvAppendBlockParams &p, int d, cudaStream_t s) {
     const dim3 g(run_columns(p.run, false), (unsigned)p.run.H_kv, 2u);
     switch (d) {
-        case 64: return launch_run(kv_append_fp8_block_kernel<T, 64>, g, s, p);
-        case 128: return launch_run(kv_append_fp8_block_kernel<T, 128>, g, s, p);
-        default: return launch_run(kv_append_fp8_block_kernel<T, 256>, g, s, p);
+        case 64: return launch_run(kv_append_fp8_block_kernel<T, 64>, g, 64, s, p);
+        case 128: return launch_run(kv_append_fp8_block_kernel<T, 128>, g, 128, s, p);
+        default: return launch_run(kv_append_fp8_block_kernel<T, 256>, g, 256, s, p);
     }
 }
 
@@ -377,9 +381,9 @@ cudaError_t read_d(const KvReadBlockParams &p, int d, cudaStream_t s) {
     while ((2 << lg) * kBlockSize * d <= 32768 && p.run.H_kv % (2 << lg) == 0) ++lg;
     const dim3 g(run_columns(p.run, p.zero_rest), (unsigned)(p.run.H_kv >> lg), 2u);
     switch (d) {
-        case 64: return launch_run(kv_read_fp8_block_kernel<T, 64>, g, s, p, lg);
-        case 128: return launch_run(kv_read_fp8_block_kernel<T, 128>, g, s, p, lg);
-        default: return launch_run(kv_read_fp8_block_kernel<T, 256>, g, s, p, lg);
+        case 64: return launch_run(kv_read_fp8_block_kernel<T, 64>, g, kRunThreads, s, p, lg);
+        case 128: return launch_run(kv_read_fp8_block_kernel<T, 128>, g, kRunThreads, s, p, lg);
+        default: return launch_run(kv_read_fp8_block_kernel<T, 256>, g, kRunThreads, s, p, lg);
     }
 }
 
