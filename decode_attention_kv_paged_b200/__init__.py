@@ -543,8 +543,8 @@ def _read_fp8_block(dev, stream, k_cache, v_cache, k_scale, v_scale, positions, 
     # rows that no sequence owns are zeros in new tensors
     rest = 1 if out is None else 0
     if out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
-        v_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        k_out = torch.empty_strided(shape, (H_kv * d, d, 1), dtype=dtype, device=k_cache.device)
+        v_out = torch.empty_like(k_out)
         ko, vo = k_out.data_ptr(), v_out.data_ptr()
     else:
         k_out, v_out = out
