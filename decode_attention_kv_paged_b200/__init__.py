@@ -646,6 +646,7 @@ def decode_gqa_fp8_block(q, k_cache, v_cache, k_scale, v_scale, seq_lens, block_
     positions (drafted tokens): query i sits at seq_lens[b] - q_len + i and
     sees the keys up to its own position, within the window and the kept first
     positions or global set (q_len 1 only).  Rows that see nothing are zero.
+    Weights are rounded to f16 before they meet V, all else is fp32.
     `workspace`: from fp8_block_workspace, not shared with a call that may run
     at the same time; without it each call takes a new one."""
     dev, handle, where = _place(q, "q", stream)

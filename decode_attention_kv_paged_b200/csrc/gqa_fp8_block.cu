@@ -13,13 +13,15 @@
 //     S^T [128 keys][rows]  = K [128][d] . Q^T        K as loaded (K-major)
 //     O^T [d][rows]         = V^T [d][128] . P        V as loaded (MN-major)
 // and the few query rows the N side, which costs least (an MMA of M = 128,
-// K = 32 takes 47 cycles for any N <= 64, measured).  A bf16 or fp32 operand
-// against 8-bit codes is split into two E4M3 columns: x = hi + lo / 32, hi =
-// RNE(x), lo = RNE(32 (x - hi)).  For Q (8 significant bits, scaled by a power
-// of two per row) that is exact down to 2^-22 of the row's largest value.  For
-// the weights it leaves 2^-8 of a weight at most (each step rounds by 2^-4, so
-// together as much as one bf16 rounding), and 2^-23 of the largest weight of
-// the tile where the pieces are subnormal.
+// K = 32 takes 47 cycles for any N <= 64, measured).  An operand of more bits
+// against 8-bit codes is split into E4M3 columns, each the rounded remainder of
+// those before it: x = a + b / 32 + c / 1024, a = RNE(x), b = RNE(32 (x - a)),
+// c = RNE(1024 (x - a - b / 32)); each holds 4 significant bits.  For Q (8 bits,
+// scaled by a power of two per row) two are exact down to 2^-22 of the row's
+// largest value.  The weights are rounded to f16 (2^-11 of a weight), which
+// three hold exactly down to 2^-14, and within 2^-28, of the tile's largest.
+// (Two left 2^-8 of a weight, the one rounding that showed beside the output's:
+// relative L2 1.8e-3 against 1.65e-3.)
 //
 // Softmax.  One thread per key; the largest score of each row comes from a
 // warp reduction and an exchange between the four warps.  A tile's weights are
@@ -71,11 +73,13 @@ struct FbCfg {
     static constexpr int kBoxes = D / kRowBytes;
     static constexpr int kHalves = D == 256 ? 2 : 1;          // M = 128 pieces of O^T
     static constexpr int kM = D == 64 ? 64 : 128;             // M of O^T
-    static constexpr int kN = 2 * NQ;                         // hi and lo columns
+    static constexpr int kN = 2 * NQ;                         // columns of S: two pieces of Q
+    // columns of P and O^T: three pieces, 16 at a time (M = 128 takes N so)
+    static constexpr int kNP = NQ == 8 ? 32 : 3 * NQ;
     static constexpr int kBoxBytes = kFbTile * kRowBytes;     // one box of a tile
     static constexpr int kSlot = kFbTile * D;
     static constexpr int kQBytes = kN * D;
-    static constexpr int kPBytes = kN * kFbTile;
+    static constexpr int kPBytes = kNP * kFbTile;
     // P and O^T buffers: four, so that the softmax seldom waits for the products
     // and the output of its earlier tiles, where tensor memory has the room.
     static constexpr int kOut = D == 256 && NQ == 32 ? 2 : 4;
@@ -93,7 +97,7 @@ struct FbCfg {
     static constexpr int kOffBar = kOffP + kOut * kPBytes;
     static constexpr int kSmem = kOffBar + 16 * 1024 + 1024;
     static constexpr uint32_t kTmemS = 0, kTmemO = 2 * kN;
-    static constexpr uint32_t kTmemUsed = 2 * kN + kOut * kHalves * kN;
+    static constexpr uint32_t kTmemUsed = 2 * kN + kOut * kHalves * kNP;
     static constexpr uint32_t kTmemCols =
         kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
     static_assert(kKStages >= 2 && kVStages >= 2, "at least two stages per ring");
@@ -174,17 +178,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
     return r;
 }
 
-// x = hi + lo / 32 for two numbers of at most 256 in size.
-__device__ __forceinline__ void e4m3_split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    const uint32_t x = pack_f16x2(a, b);
-    hi = f16x2_to_e4m3x2(x);
-    const uint32_t back = e4m3x2_to_f16x2(hi);
-    const __half2 k = __floats2half2_rn(32.f, 32.f);
-    // the difference has few bits: exact in f16
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x),
-                              *reinterpret_cast<const __half2 *>(&back));
-    const __half2 r = __hmul2(d, k);
-    lo = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t *>(&r));
+// The first E4M3 piece of two f16 numbers of at most 256 in size; x becomes 32
+// times what is left (at most 256 again; few bits: exact in f16).
+__device__ __forceinline__ uint32_t e4m3_piece(uint32_t &x) {
+    const uint32_t c = f16x2_to_e4m3x2(x), back = e4m3x2_to_f16x2(c);
+    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&x),
+                                      *reinterpret_cast<const __half2 *>(&back)),
+                              __floats2half2_rn(32.f, 32.f));
+    x = *reinterpret_cast<const uint32_t *>(&r);
+    return c;
 }
 
 // UMMA shared-memory descriptor; layout 0: no swizzle, 2: 128-byte, 4: 64-byte.
@@ -420,7 +422,9 @@ __device__ __noinline__ void fb_prepare_q(const unsigned char *raw, unsigned cha
         uint32_t hi[kE / 2], lo[kE / 2];
 #pragma unroll
         for (int j = 0; j < kE / 2; ++j) {
-            e4m3_split2(bf16lo(w[j]) * by, bf16hi(w[j]) * by, hi[j], lo[j]);
+            uint32_t x = pack_f16x2(bf16lo(w[j]) * by, bf16hi(w[j]) * by);
+            hi[j] = e4m3_piece(x);
+            lo[j] = f16x2_to_e4m3x2(x);
             if (top >= 0x7F800000u) hi[j] = 0x7F7Fu;
         }
 #pragma unroll
@@ -760,7 +764,7 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
         __syncwarp();
     } else if (warp == 2) {
         // ====================================================== O^T = V^T P
-        constexpr uint32_t idesc = fb_idesc(C::kM, C::kN, 1, 1);
+        constexpr uint32_t idesc = fb_idesc(C::kM, C::kNP, 1, 1);
         constexpr int kLayout = C::kRowBytes == 128 ? 2 : 4;
         const uint64_t dv = fb_desc(smem_u32(sV), 16, C::kRowBytes * 8, kLayout);
         const uint64_t dp = fb_desc(smem_u32(sP), 128, 2048, 0);
@@ -778,14 +782,14 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (n >= C::kOut && !wait(&sh->o_free[buf], par ^ 1u)) break;
             if (!wait(&sh->p_full[buf], par)) break;
             tc_fence_after();
-            const uint32_t d = tmem + C::kTmemO + buf * (C::kHalves * C::kN);
+            const uint32_t d = tmem + C::kTmemO + buf * (C::kHalves * C::kNP);
             const uint64_t a0 = dv + ((vs * C::kSlot) >> 4);
             const uint64_t b0 = dp + ((buf * C::kPBytes) >> 4);
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
                 for (int s = 0; s < kFbTile / 32; ++s)
-                    umma_f8(lead, d + h * C::kN,
+                    umma_f8(lead, d + h * C::kNP,
                             a0 + ((h * C::kBoxBytes + s * 32 * C::kRowBytes) >> 4),
                             b0 + ((s * 512) >> 4), idesc, s != 0);
             umma_commit_by(lead, &sh->o_full[buf]);
@@ -994,7 +998,7 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                 for (int q = 0; q < R; q += 2)
                     l[q / 2] = __fmul2_rn(l[q / 2], *reinterpret_cast<const float2 *>(grow + q));
             }
-            uint32_t hi[R / 4], lo[R / 4];
+            uint32_t pa[R / 4], pb[R / 4], pc[R / 4];              // the pieces
 #pragma unroll
             for (int q = 0; q < R; q += 4) {
                 const float4 r = *reinterpret_cast<const float4 *>(ref + q);
@@ -1007,21 +1011,23 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                 y.y = exp2_approx(y.y);
                 l[q / 2] = __ffma2_rn(x, make_float2(f.x, f.y), l[q / 2]);
                 l[q / 2 + 1] = __ffma2_rn(y, make_float2(f.z, f.w), l[q / 2 + 1]);
-                uint32_t hx, lx, hy, ly;
-                e4m3_split2(x.x, x.y, hx, lx);
-                e4m3_split2(y.x, y.y, hy, ly);
-                hi[q / 4] = __byte_perm(hx, hy, 0x5410);
-                lo[q / 4] = __byte_perm(lx, ly, 0x5410);
+                uint32_t u = pack_f16x2(x.x, x.y), v = pack_f16x2(y.x, y.y);
+                pa[q / 4] = __byte_perm(e4m3_piece(u), e4m3_piece(v), 0x5410);
+                pb[q / 4] = __byte_perm(e4m3_piece(u), e4m3_piece(v), 0x5410);
+                pc[q / 4] = __byte_perm(f16x2_to_e4m3x2(u), f16x2_to_e4m3x2(v), 0x5410);
             }
             // 16 columns of a key are 16 bytes, keys one after another
             unsigned char *pk = sP + ob * C::kPBytes + key * 16;
             if constexpr (NQ == 8) {
-                *reinterpret_cast<uint4 *>(pk) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+                *reinterpret_cast<uint4 *>(pk) = make_uint4(pa[0], pa[1], pb[0], pb[1]);
+                *reinterpret_cast<uint4 *>(pk + 2048) = make_uint4(pc[0], pc[1], 0u, 0u);
             } else {
+                constexpr int kPiece = (NQ / 16) * 2048;
                 pk += kSplit ? grp * 2048 : 0;
-                *reinterpret_cast<uint4 *>(pk) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(pk + (NQ / 16) * 2048) =
-                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                *reinterpret_cast<uint4 *>(pk) = make_uint4(pa[0], pa[1], pa[2], pa[3]);
+                *reinterpret_cast<uint4 *>(pk + kPiece) = make_uint4(pb[0], pb[1], pb[2], pb[3]);
+                *reinterpret_cast<uint4 *>(pk + 2 * kPiece) =
+                    make_uint4(pc[0], pc[1], pc[2], pc[3]);
             }
             if (tile.flags & (kSplit ? kFbLast : kFbLastPair)) {    // the group's last of the part
                 float v[R];
@@ -1080,27 +1086,42 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
                 for (int c0 = 0; c0 < NQ; c0 += kCols) {
-                    float xy[2 * kCols];
-                    const uint32_t at = tmem + C::kTmemO + (buf * C::kHalves + h) * C::kN + tlane;
-                    if constexpr (NQ <= 16) {
-                        fb_tmem_ld<2 * kCols>(at, xy);
+                    // the pieces of kCols columns, the last first (of 16, two at a
+                    // time: registers are short)
+                    float2 x[kCols / 2];
+                    const uint32_t at =
+                        tmem + C::kTmemO + (buf * C::kHalves + h) * C::kNP + c0 + tlane;
+                    if constexpr (NQ == 8) {
+                        float t[32];
+                        tmem_ld32(at, t);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 yz = __ffma2_rn(make_float2(t[16 + 2 * q], t[17 + 2 * q]),
+                                                         piece,
+                                                         make_float2(t[8 + 2 * q], t[9 + 2 * q]));
+                            x[q] = __ffma2_rn(yz, piece, make_float2(t[2 * q], t[2 * q + 1]));
+                        }
                     } else {
-                        tmem_ld16(at + c0, xy);
-                        tmem_ld16(at + NQ + c0, xy + 16);
+                        float t[16];
+                        tmem_ld16(at + 2 * NQ, t);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) x[q] = make_float2(t[2 * q], t[2 * q + 1]);
+#pragma unroll
+                        for (int part = 1; part >= 0; --part) {
+                            tmem_ld16(at + part * NQ, t);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                x[q] = __ffma2_rn(x[q], piece, make_float2(t[2 * q], t[2 * q + 1]));
+                        }
                     }
 #pragma unroll
                     for (int q = 0; q < kCols; q += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(join + c0 + q);
                         const float4 k = *reinterpret_cast<const float4 *>(keep + c0 + q);
-                        const float *x = xy + q, *y = xy + kCols + q;
                         float2 *d = &o[h][(c0 + q) / 2];
-                        d[0] = __ffma2_rn(__ffma2_rn(make_float2(y[0], y[1]), piece,
-                                                     make_float2(x[0], x[1])),
-                                          make_float2(f.x, f.y),
+                        d[0] = __ffma2_rn(x[q / 2], make_float2(f.x, f.y),
                                           __fmul2_rn(d[0], make_float2(k.x, k.y)));
-                        d[1] = __ffma2_rn(__ffma2_rn(make_float2(y[2], y[3]), piece,
-                                                     make_float2(x[2], x[3])),
-                                          make_float2(f.z, f.w),
+                        d[1] = __ffma2_rn(x[q / 2 + 1], make_float2(f.z, f.w),
                                           __fmul2_rn(d[1], make_float2(k.z, k.w)));
                     }
                 }

@@ -490,7 +490,11 @@ int kv_read_fp8_block(const void *k_cache, const void *v_cache, const float *k_s
  * q_len + 62.  A query that sees no key (T_b < q_len - i) gets a zero row.
  * q [B][q_len][H_q][d] bf16, q_stride elements (>= H_q * d, a multiple of 8)
  * from one position's heads to the next; out [B][q_len][H_q][d] bf16,
- * contiguous; scale finite.  Scales in the cache: 0, or positive and within
+ * contiguous; scale finite.  Rounding: q and the codes enter as they are;
+ * each softmax weight is rounded to f16 (2^-11 of it; weights below 2^-14 of
+ * the largest of their 128 keys by 2^-28 of that one) before it meets V;
+ * scores, sums and outputs before the last rounding are fp32.
+ * Scales in the cache: 0, or positive and within
  * [2^-64, 2^64] for full precision; a block's scale of 0 makes its values 0
  * (not its weight).  Codes in rows that no query of the sequence sees may
  * be anything, NaN included; a NaN in a row that one query of the sequence
