@@ -60,11 +60,11 @@ struct GqaFp8BlockParams {
     int num_ctas;
     unsigned long long timeout_ns;
     // filled by the launch: the query rows of a K/V head (group x q_len) in
-    // chunks of chunk_rows; partials [2 num_ctas][columns][d] with their
-    // reference and sum
+    // chunks of chunk_rows; partials [2 num_ctas][columns][d] with what they
+    // are relative to, the largest score, and the sum of weights relative to it
     int chunk_rows, chunks;
     float *ws_o;
-    float2 *ws_ml;
+    float4 *ws_ml;
     FbCut *ws_cut;                // the unit cut at each CTA's end
     bool whole_units;             // one CTA per unit, nothing split
     bool small_plan;              // few sequences, a list that 32 bits count

@@ -24,12 +24,17 @@
 // relative L2 1.8e-3 against 1.65e-3.)
 //
 // Softmax.  One thread per key; the largest score of each row comes from a
-// warp reduction and an exchange between the four warps.  A tile's weights are
-// taken relative to its own largest (weight x V scale), not to a running one:
-// the two E4M3 pieces then lose nothing to a key far ahead in another tile.
-// The tile's O^T is read from tensor memory and added to fp32 registers with
-// the factor that brings it to the running reference.  Sums of weights stay in
-// fp32 registers, per key lane, until the unit's end.
+// warp reduction and an exchange between the four warps.  Two references, as
+// the sum of the weights knows nothing of V scales: exponentials are taken
+// relative to the block's own largest score.  With one factor a row they join
+// the sum of weights, relative to the running largest score; with another they
+// become the operand P, relative to the tile's largest (weight x V scale), not
+// a running one: the E4M3 pieces then lose nothing to a key far ahead in
+// another tile.  Both factors are at most 1 for any V scales, so that blocks
+// 2^240 apart stand beside one another.  The tile's O^T is read from tensor
+// memory and added to fp32 registers with the factor that brings it to its
+// running reference; sums of weights stay in fp32 registers, per key lane,
+// until the unit's end, where the two references meet.
 //
 // Roles (one CTA per SM, 16 warps): warp 0 loads tiles of two blocks by TMA
 // (swizzled as the MMA reads them) into two rings, and writes a record of each
@@ -138,19 +143,19 @@ struct FbShared {
     alignas(16) FbTile tile[kFbRing];
     alignas(16) FbPart part[kFbRing];
     // Per tile and block: K scale x softmax scale (log2 units), log2 of the V
-    // scale, its reciprocal, 0 where the V scale is 0.
+    // scale (of 0: -inf), 0 where there is no block.
     alignas(16) float4 info[kFbRing][2];
     alignas(16) float qsc[kFbRing][NQ];    // power-of-two scale of each query row
     alignas(16) int row_at[kFbRing][NQ];   // its position
     // per softmax group, on even and odd turns: largest scores per warp
     alignas(16) float wmax[2][2][4][kRows];
-    // Per softmax warp: what the weights are relative to (negative), their
-    // factor in the sum, the factor of the sum so far.
-    alignas(16) float ref[8][kRows], fac[8][kRows], grow[8][kRows];
-    alignas(16) float top[4][NQ];  // a tile's largest score (with its V scale)
+    // Per softmax warp: what the exponentials are relative to (negative), their
+    // factors in the sum and in P, the factor of the sum so far.
+    alignas(16) float ref[8][kRows], fac[8][kRows], pfac[8][kRows], grow[8][kRows];
+    alignas(16) float top[4][NQ];  // a tile's largest score with its V scale
     alignas(16) float join[4][2][NQ];   // per output warp: factor of the tile, of the rest
-    // at a part's end, per softmax group that had a tile: sums of weights, what
-    // they are relative to (row split: the first group's place holds all rows)
+    // at a part's end, per softmax group that had a tile: sums of weights, the
+    // scores they are relative to (row split: the first group's place holds all rows)
     float lsum[4][2][4][NQ];
     float ltop[4][2][NQ];
     uint32_t tmem_base;
@@ -656,14 +661,11 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // The scales may arrive after the copies set out: the arrival
                 // that lets others see the tile comes behind them.
                 if (lane == j || lane == j + 1) {
-                    // A scale of 0 makes the values 0, not the weights: they
-                    // enter the sum through any other scale.
-                    const float vse = my_vs == 0.f ? 5.421010862427522e-20f /* 2^-64 */ : my_vs;
                     sh->info[tile % kFbRing][lane - j] =
                         my_block && lane < count
-                            ? make_float4(my_ks * p.scale_log2, log2f(vse), 1.f / vse,
-                                          my_vs == 0.f ? 0.f : 1.f)
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                            ? make_float4(my_ks * p.scale_log2,
+                                          my_vs == 0.f ? -INFINITY : log2f(my_vs), 1.f, 0.f)
+                            : make_float4(0.f, -INFINITY, 0.f, 0.f);
                 }
                 __syncwarp();
                 if (lane == 0) {
@@ -854,12 +856,13 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int key = 32 * w + lane;                         // of the tile
         const uint32_t tlane = (uint32_t)(32 * w) << 16;
         const int L = p.q_len, sink = p.vis.sink;
-        float *ref = sh->ref[warp - 4], *fac = sh->fac[warp - 4], *grow = sh->grow[warp - 4];
+        float *ref = sh->ref[warp - 4], *fac = sh->fac[warp - 4], *pfac = sh->pfac[warp - 4],
+              *grow = sh->grow[warp - 4];
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return fb_wait(bar, parity, p, abort_flag);
         };
         float2 l[R / 2];
-        float top = -INFINITY;                                 // of row q0 + lane
+        float top = -INFINITY;                                 // largest score of row q0 + lane
         int seg = -1, turns = 0;                               // tiles of this group so far
         for (int n = kSplit ? 0 : grp, left = walk.rest;; n += kStep, ++turns) {
             if (!kSplit && n > 0) {
@@ -887,12 +890,14 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             const int T = part.T, window = part.window;
             const int first = (half ? tile.pos[1] : tile.pos[0]) + 32 * (w & 1);
             const int pos = first + lane;
-            const bool there = half == 0 || (tile.flags & kFbTwo);   // this warp's block
+            // this warp's block, and whether its values are 0
+            const bool there = (half == 0 || (tile.flags & kFbTwo)) && info.z != 0.f;
+            const bool zero = info.y == -INFINITY;
             // every key of the warp seen by every query
             const bool all = there && first + 31 <= T - L &&
                              (window <= 0 || first > T - 1 - window || first + 31 < sink);
             bool early = window <= 0 || pos < sink;             // whatever the window
-            if (!all || info.w == 0.f) {
+            if (!all || zero) {
                 if (G && there && window > 0 && first <= T - 1 - window)
                     early |= (global_mask(p.vis, part.b, first / kBlockSize, lane) >> (pos & 63)) &
                              1ull;
@@ -901,7 +906,7 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // scale is 0.  (Row split: either group zeroes half of a row.)
                 const int vs = n % C::kVStages;
                 if (!wait(&sh->v_full[vs], (uint32_t)((n / C::kVStages) & 1))) break;
-                if (!(there && pos < T && info.w != 0.f && (early || pos > T - L - window))) {
+                if (!(there && pos < T && !zero && (early || pos > T - L - window))) {
                     constexpr int kZero = C::kRowBytes / 16 / (kSplit ? 2 : 1);
                     uint4 *v = reinterpret_cast<uint4 *>(sV + vs * C::kSlot +
                                                          key * C::kRowBytes) +
@@ -926,20 +931,19 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 tc_fence_before();
                 mbar_arrive_warp(&sh->s_free[buf]);
-                // scores in log2 units, the V scale's exponent among them
+                // scores in log2 units
                 const float2 k2 = make_float2(info.x, info.x);
-                const float2 v2 = make_float2(info.y, info.y);
                 const float2 piece = make_float2(0.03125f, 0.03125f);
                 const float *qsc = &sh->qsc[seg % kFbRing][q0], *y = x + R;
 #pragma unroll
                 for (int q = 0; q < R; q += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(qsc + q);
-                    s[q / 2] = __ffma2_rn(__ffma2_rn(make_float2(y[q], y[q + 1]), piece,
+                    s[q / 2] = __fmul2_rn(__ffma2_rn(make_float2(y[q], y[q + 1]), piece,
                                                      make_float2(x[q], x[q + 1])),
-                                          __fmul2_rn(make_float2(f.x, f.y), k2), v2);
-                    s[q / 2 + 1] = __ffma2_rn(__ffma2_rn(make_float2(y[q + 2], y[q + 3]), piece,
+                                          __fmul2_rn(make_float2(f.x, f.y), k2));
+                    s[q / 2 + 1] = __fmul2_rn(__ffma2_rn(make_float2(y[q + 2], y[q + 3]), piece,
                                                          make_float2(x[q + 2], x[q + 3])),
-                                              __fmul2_rn(make_float2(f.z, f.w), k2), v2);
+                                              __fmul2_rn(make_float2(f.z, f.w), k2));
                 }
             }
             if (!all) {
@@ -958,7 +962,7 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             // The P buffer, and what goes with it, is free again (long ago, as a
             // rule: tested here, where the scores' arithmetic hides it).
             if (n >= C::kOut && !wait(&sh->o_free[ob], (uint32_t)((n / C::kOut - 1) & 1))) break;
-            // largest of the tile, per row (every lane has it: one writes)
+            // largest of the warp's keys, per row (every lane has it: one writes)
             {
                 float m[R];
 #pragma unroll
@@ -978,18 +982,22 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             bool grew = false;
             if (lane < R) {
                 const float(*wm)[R] = sh->wmax[grp][turns & 1];
-                const float m =
-                    fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
-                const float now = m != m ? m : fmaxf(top, m);
-                // factor of this tile's weights (2^8 in them) in the sum
-                const float c = m == -INFINITY ? 0.f : exp2_approx(m - now - 8.f);
+                const float m0 = fmaxf(wm[0][lane], wm[1][lane]);    // of either block
+                const float m1 = fmaxf(wm[2][lane], wm[3][lane]);
+                const float m = half ? m1 : m0, both = fmaxf(m0, m1);
+                const float now = both != both ? both : fmaxf(top, both);
+                const float v0 = m0 + sh->info[n % kFbRing][0].y;    // with their V scales
+                const float v1 = m1 + sh->info[n % kFbRing][1].y;
+                const float v = half ? v1 : v0, most = fmaxf(v0, v1);
                 const float a = top == now ? 1.f : exp2_approx(top - now);
+                // 2^8 is in the exponentials; P keeps it
                 ref[lane] = m == -INFINITY ? 0.f : 8.f - m;
-                fac[lane] = c * info.z;
+                fac[lane] = m == -INFINITY ? 0.f : exp2_approx(m - now - 8.f);
+                pfac[lane] = v == -INFINITY ? 0.f : v == most ? 1.f : exp2_approx(v - most);
                 grow[lane] = a;
                 grew = a != 1.f;
                 top = now;
-                if (w == 0) sh->top[ob][q0 + lane] = m;
+                if (w == 0) sh->top[ob][q0 + lane] = most;
             }
             grew = __any_sync(0xffffffffu, grew);
             __syncwarp();
@@ -1003,6 +1011,7 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             for (int q = 0; q < R; q += 4) {
                 const float4 r = *reinterpret_cast<const float4 *>(ref + q);
                 const float4 f = *reinterpret_cast<const float4 *>(fac + q);
+                const float4 g = *reinterpret_cast<const float4 *>(pfac + q);
                 float2 x = __fadd2_rn(s[q / 2], make_float2(r.x, r.y));
                 float2 y = __fadd2_rn(s[q / 2 + 1], make_float2(r.z, r.w));
                 x.x = exp2_approx(x.x);
@@ -1011,6 +1020,8 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                 y.y = exp2_approx(y.y);
                 l[q / 2] = __ffma2_rn(x, make_float2(f.x, f.y), l[q / 2]);
                 l[q / 2 + 1] = __ffma2_rn(y, make_float2(f.z, f.w), l[q / 2 + 1]);
+                x = __fmul2_rn(x, make_float2(g.x, g.y));
+                y = __fmul2_rn(y, make_float2(g.z, g.w));
                 uint32_t u = pack_f16x2(x.x, x.y), v = pack_f16x2(y.x, y.y);
                 pa[q / 4] = __byte_perm(e4m3_piece(u), e4m3_piece(v), 0x5410);
                 pb[q / 4] = __byte_perm(e4m3_piece(u), e4m3_piece(v), 0x5410);
@@ -1072,7 +1083,7 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (lane < NQ) {
                 const float m = sh->top[buf][lane];
                 const float now = m != m ? m : fmaxf(top, m);
-                // a tile that the row does not see adds nothing
+                // a tile that the row does not see, or whose values are 0, adds nothing
                 join[lane] = m == -INFINITY ? 0.f : exp2_approx(m - now - 8.f);
                 keep[lane] = top == now ? 1.f : exp2_approx(top - now);
                 top = now;
@@ -1128,34 +1139,45 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (tile.flags & kFbLast) {
                 const int seg = tile.flags >> kFbSegShift;
                 const FbPart part = sh->part[seg % kFbRing];
-                float sum = 0.f;                               // of row `lane`
+                float sum = 0.f, high = -INFINITY;             // of row `lane`
                 int out_row = 0;
                 if (lane < part.rows) {
+                    // the sum, relative to the row's largest score, of the groups
+                    // that have a tile of this part
+                    constexpr int kGroups = FbShared<NQ>::kRowSplit ? 1 : 2;
+                    float lt[kGroups];
 #pragma unroll
-                    for (int g = 0; g < (FbShared<NQ>::kRowSplit ? 1 : 2); ++g) {
-                        // the group has a tile of this part
-                        if (!FbShared<NQ>::kRowSplit && n == n0 && (n & 1) != g) continue;
-                        const float lt = sh->ltop[seg & 3][g][lane];
+                    for (int g = 0; g < kGroups; ++g) {
+                        lt[g] = kGroups == 2 && n == n0 && (n & 1) != g
+                                    ? -INFINITY
+                                    : sh->ltop[seg & 3][g][lane];
+                        high = fmaxf(high, lt[g]);
+                    }
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
                         const float *ls = &sh->lsum[seg & 3][g][0][lane];
                         const float s = (ls[0] + ls[NQ]) + (ls[2 * NQ] + ls[3 * NQ]);
-                        if (lt != -INFINITY) sum = fmaf(s, exp2_approx(lt - top), sum);
+                        if (lt[g] != -INFINITY) sum = fmaf(s, exp2_approx(lt[g] - high), sum);
                     }
                     const int row = part.row0 + lane, i = row / p.group;
                     out_row = (part.b * p.q_len + i) * p.H_q + part.kvh * p.group +
                               (row - i * p.group);
                 }
                 if (part.whole) {
+                    // two factors: their product may be too small for fp32
                     const float by = sum != 0.f ? 1.f / sum : 0.f;
+                    const float over = sum != 0.f ? exp2f(top - high) : 0.f;
                     __nv_bfloat16 *dst = p.out + col;
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
                         const float f = __shfl_sync(0xffffffffu, by, q);
+                        const float e = __shfl_sync(0xffffffffu, over, q);
                         const int r = __shfl_sync(0xffffffffu, out_row, q);
                         if (q < part.rows && mine) {
 #pragma unroll
                             for (int h = 0; h < C::kHalves; ++h)
                                 dst[(size_t)r * D + h * 128] = __float2bfloat16_rn(
-                                    (q & 1 ? o[h][q / 2].y : o[h][q / 2].x) * f);
+                                    (q & 1 ? o[h][q / 2].y : o[h][q / 2].x) * f * e);
                         }
                     }
                 } else {
@@ -1169,7 +1191,7 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
                                 dst[q * D + h * 128] = q & 1 ? o[h][q / 2].y : o[h][q / 2].x;
                         }
                     if (w == 0 && lane < part.rows)
-                        p.ws_ml[slot * NQ + lane] = make_float2(top, sum);
+                        p.ws_ml[slot * NQ + lane] = make_float4(top, high, sum, 0.f);
                 }
             }
             tc_fence_before();
@@ -1205,6 +1227,7 @@ __global__ void __launch_bounds__(kFbJoinThreads)
 gqa_fp8_block_join_kernel(const GqaFp8BlockParams p) {
     constexpr int kC = D / 4, kAhead = 8;
     extern __shared__ __align__(16) unsigned char join_smem[];
+    __shared__ float2 s_by[NQ];
     pdl_wait_primary();
     pdl_launch_dependents();
     const FbCut cut = p.ws_cut[blockIdx.x];
@@ -1217,26 +1240,28 @@ gqa_fp8_block_join_kernel(const GqaFp8BlockParams p) {
     float *s_w = reinterpret_cast<float *>(s_o + kFbJoinThreads);         // [rows][n]
     auto slot = [&](int k) { return (size_t)(k == 0 ? cut.slot : 2 * (cut.first + k)) * NQ; };
     for (int q = warp; q < u.rows; q += kFbJoinThreads / 32) {
-        float top = -INFINITY, sum = 0.f;
+        float top = -INFINITY, high = -INFINITY, sum = 0.f;
         bool nan = false;
         for (int k = lane; k < n; k += 32) {
-            const float t = __ldcg(&p.ws_ml[slot(k) + q].x);
-            nan |= t != t;
-            top = fmaxf(top, t);
+            const float4 ml = __ldcg(p.ws_ml + slot(k) + q);
+            nan |= ml.x != ml.x || ml.y != ml.y;
+            top = fmaxf(top, ml.x);
+            high = fmaxf(high, ml.y);
         }
         nan = __any_sync(0xffffffffu, nan);
         top = nan ? NAN : warp_max(top);
+        high = nan ? NAN : warp_max(high);
         for (int k = lane; k < n; k += 32) {
-            const float2 ml = __ldcg(p.ws_ml + slot(k) + q);
-            // a split whose keys the row does not see adds nothing
-            const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
-            s_w[q * n + k] = f;
-            sum = fmaf(f, ml.y, sum);
+            const float4 ml = __ldcg(p.ws_ml + slot(k) + q);
+            // a split whose keys the row does not see adds nothing, one whose
+            // values are 0 its weights
+            s_w[q * n + k] = ml.x == -INFINITY ? 0.f : exp2f(ml.x - top);
+            if (ml.y != -INFINITY) sum = fmaf(exp2f(ml.y - high), ml.z, sum);
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float by = sum != 0.f ? 1.f / sum : 0.f;
-        for (int k = lane; k < n; k += 32) s_w[q * n + k] *= by;
+        if (lane == 0)
+            s_by[q] = sum != 0.f ? make_float2(1.f / sum, exp2f(top - high)) : make_float2(0.f, 0.f);
     }
     __syncthreads();
     // Threads of an item: a power of two, while each still has splits to add.
@@ -1276,8 +1301,9 @@ gqa_fp8_block_join_kernel(const GqaFp8BlockParams p) {
         }
         if (sub == 0 && it < items) {
             const int row = u.row0 + q, i = row / p.group, g = row % p.group;
-            __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x, o.y),
-                                   __floats2bfloat162_rn(o.z, o.w)};
+            const float2 by = s_by[q];
+            __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x * by.x * by.y, o.y * by.x * by.y),
+                                   __floats2bfloat162_rn(o.z * by.x * by.y, o.w * by.x * by.y)};
             *reinterpret_cast<uint2 *>(p.out + ((size_t)(cut.b * p.q_len + i) * p.H_q +
                                                 u.kvh * p.group + g) * D + c) =
                 *reinterpret_cast<const uint2 *>(w);
@@ -1294,10 +1320,10 @@ int fp8_block_rows(int rows) {
 
 static int fb_columns(int chunk_rows) { return chunk_rows <= 8 ? 8 : chunk_rows <= 16 ? 16 : 32; }
 
-// The workspace: cuts, partials, their references and sums.
+// The workspace: cuts, partials, their two references and sums.
 int64_t fp8_block_workspace_bytes(int num_ctas, int rows, int d) {
     const int64_t nq = fb_columns(fp8_block_rows(rows));
-    return (int64_t)sizeof(FbCut) * kFp8BlockMaxCtas + 2ll * num_ctas * nq * (d * 4 + 8);
+    return (int64_t)sizeof(FbCut) * kFp8BlockMaxCtas + 2ll * num_ctas * nq * (d * 4 + 16);
 }
 
 namespace {
@@ -1374,7 +1400,7 @@ cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &given, int d, void *wo
     const size_t slots = 2 * (size_t)p.num_ctas * fb_columns(p.chunk_rows);
     p.ws_cut = static_cast<FbCut *>(workspace);
     p.ws_o = reinterpret_cast<float *>(p.ws_cut + kFp8BlockMaxCtas);
-    p.ws_ml = reinterpret_cast<float2 *>(p.ws_o + slots * d);
+    p.ws_ml = reinterpret_cast<float4 *>(p.ws_o + slots * d);
     // Where no sequence can be long and there is an SM for every unit, a unit
     // is not split: that saves the plan and the second kernel.  Measured with
     // 32 units of 4 rows, d = 128: 8.5 us against 20.6 at 512 tokens, 16.5

@@ -494,9 +494,10 @@ int kv_read_fp8_block(const void *k_cache, const void *v_cache, const float *k_s
  * each softmax weight is rounded to f16 (2^-11 of it; weights below 2^-14 of
  * the largest of their 128 keys by 2^-28 of that one) before it meets V;
  * scores, sums and outputs before the last rounding are fp32.
- * Scales in the cache: 0, or positive and within
- * [2^-64, 2^64] for full precision; a block's scale of 0 makes its values 0
- * (not its weight).  Codes in rows that no query of the sequence sees may
+ * Scales in the cache: 0 or positive normal numbers.  V scales may lie any
+ * distance apart (all that kv_append_fp8_block leaves, 2^-126 to 2^120, in one
+ * sequence); a block's scale of 0 makes its values 0 (not its weight).  K
+ * scales have to leave a row's largest |q| * K scale * scale finite.  Codes in rows that no query of the sequence sees may
  * be anything, NaN included; a NaN in a row that one query of the sequence
  * sees may reach that sequence's other queries.
  * workspace: device memory of at least attn_decode_gqa_fp8_block_workspace
