@@ -26,6 +26,26 @@ struct BlockRun {
     bool replaced;  // a later block of the run takes the slot
 };
 
+// First global slot of sequence b that names block blk (the first position of
+// its global set in it), -1: none.  One warp, all 32 lanes; rows of up to 64.
+__device__ __forceinline__ int named_slot(const Visibility &v, int b, int blk) {
+    const int32_t *g = global_row(v, b);
+    const int lane = threadIdx.x & 31;
+    int prev = -1;                             // the entry before the 32 looked at
+    for (int k0 = 0; k0 < v.n_g; k0 += 32) {
+        const int pos = k0 + lane < v.n_g ? g[k0 + lane] : -1;
+        const int up = __shfl_up_sync(0xffffffffu, pos, 1);
+        // the row ends at the first entry that does not exceed the one before
+        const unsigned stop = __ballot_sync(0xffffffffu, pos <= (lane ? up : prev));
+        const unsigned hit = __ballot_sync(0xffffffffu, pos / kBlockSize == blk) &
+                             (stop ? (stop & (0u - stop)) - 1u : 0xffffffffu);
+        if (hit) return k0 + __ffs(hit) - 1;
+        if (stop) return -1;
+        prev = __shfl_sync(0xffffffffu, pos, 31);
+    }
+    return -1;
+}
+
 // The part of a run that CTA column x of the grid works on.  Sequence b owns
 // columns offsets[b] / 64 + 2 b and on, up to the next sequence's: a run of n
 // rows touches at most (n + 62) / 64 + 1 blocks, which is never more than the
@@ -36,8 +56,14 @@ struct BlockRun {
 // CTA gets the same answer; false where the column has no work.  flag: this
 // thread reports what is wrong with the run.  rest: the rows behind the last
 // sequence are handed out as a run without blocks.
+//
+// In a ring with a global set a block that holds a global position has a slot
+// of its own, which names it also when the ring has moved past it.  A reader
+// goes there.  A writer goes there for the blocks that lie before the window
+// when the run is done (the decode then reads them there, and a run longer than
+// the ring replaces them itself), else through the ring like kv_append_ext.
 __device__ __forceinline__ bool locate_run(const KvRunParams &p, int x, bool flag, bool rest,
-                                           BlockRun *out) {
+                                           bool reading, BlockRun *out) {
     const int lane = threadIdx.x & 31;
     int b, o0, n, ord, pos;
     if (p.offsets) {
@@ -95,13 +121,22 @@ __device__ __forceinline__ bool locate_run(const KvRunParams &p, int x, bool fla
     const int lead = pos % kBlockSize, blk = pos / kBlockSize + ord;
     const int last = (int)(((long long)pos + n - 1) / kBlockSize);
     if (blk > last) return false;
-    const int slot = table_slot(p.vis, blk);
+    int slot = table_slot(p.vis, blk);
+    bool replaced = p.vis.ring > 0 && slot >= ring_base(p.vis) && blk + p.vis.ring <= last;
+    if (p.vis.ring > 0 && p.vis.n_g > 0 &&
+        (reading || blk < window_lo(p.vis, pos + n) / kBlockSize)) {
+        const int named = named_slot(p.vis, b, blk);
+        if (named >= 0) {
+            slot = named;
+            replaced = false;
+        }
+    }
     *out = BlockRun{b,
                     o0 + (ord == 0 ? 0 : ord * kBlockSize - lead),
                     ord == 0 ? lead : 0,
                     min(kBlockSize, lead + n - ord * kBlockSize),
                     slot < p.max_blocks ? slot : -1,
-                    p.vis.ring > 0 && slot >= ring_base(p.vis) && blk + p.vis.ring <= last};
+                    replaced};
     return true;
 }
 
@@ -202,7 +237,7 @@ kv_append_fp8_block_kernel(const KvAppendBlockParams p) {
     pdl_launch_dependents();
     BlockRun br;
     const bool flag = tid == 0 && h == 0 && !is_v;
-    if (!locate_run(p.run, blockIdx.x, flag, false, &br)) return;
+    if (!locate_run(p.run, blockIdx.x, flag, false, false, &br)) return;
     const T *src = static_cast<const T *>(is_v ? p.v_new : p.k_new);
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
     const int col = (tid % kTpr) * kE, row0 = tid / kTpr;
@@ -310,7 +345,7 @@ kv_read_fp8_block_kernel(const KvReadBlockParams p, int heads_log2) {
     }
     BlockRun br;
     const bool flag = tid == 0 && blockIdx.y == 0 && !is_v;
-    if (!locate_run(p.run, blockIdx.x, flag, p.zero_rest, &br)) return;
+    if (!locate_run(p.run, blockIdx.x, flag, p.zero_rest, true, &br)) return;
     const int phys = run_block(p.run, br, flag, true);
     dst += ((int64_t)br.src - br.r0) * (int64_t)pitch;
     if (phys < 0) {

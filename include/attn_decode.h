@@ -443,7 +443,10 @@ int attn_mla_project_out(const void *z, const void *u_v, void *o, int B, int H, 
  *   codes:  RNE(x / s), saturated to +-448 (infinities too); a NaN stays NaN.
  * Rows of a block behind the written ones are left as they were.  Where a run
  * is longer than a ring table, the blocks that a later block of the same run
- * replaces are not written.  A block may be written by one sequence of a call
+ * replaces are not written; with a global set, a block that holds a global
+ * position and lies before the window once the run is done (T = positions[b] +
+ * rows) is written through its global slot, where the decode reads it (the
+ * caller gives the ring slot a new block, as between single tokens).  A block may be written by one sequence of a call
  * only (no order between two), and scales found in the cache must be 0 or
  * powers of two of at least 2^-126.
  * k_new, v_new [n_tokens][H_kv][d], bf16 or fp32 (dtype), 16-byte aligned;
@@ -466,7 +469,12 @@ int kv_append_fp8_block(const void *k_new, const void *v_new, int64_t k_stride, 
  * v_out [n_tokens][H_kv][d] (bf16 or fp32, contiguous, 16-byte aligned) gets
  * code_value * block scale, rounded to nearest even, of position positions[b]
  * + t of sequence b (for prefix reuse by a dense prefill, cache migration,
- * checks).  Arguments as for kv_append_fp8_block.  Positions that the table
+ * checks).  Arguments as for kv_append_fp8_block.  In a ring table with a
+ * global set a block that holds a global position is read through its global
+ * slot, which names it whether or not the ring still holds it.  Other positions
+ * of a ring have to be ones that it still holds: which these are depends on
+ * what was appended, which this call does not know, and the rows of a later
+ * block come back where the ring has moved on.  Positions that the table
  * row cannot name, whose block id is outside the pool, or whose ring slot a
  * later position of the same run holds, read as zeros and are flagged
  * (ATTN_ERR_BAD_BLOCK).  Output rows that belong to no sequence (before
