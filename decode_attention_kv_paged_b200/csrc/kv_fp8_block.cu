@@ -52,7 +52,9 @@ __device__ __forceinline__ int named_slot(const Visibility &v, int b, int blk) {
 // floor(o' / 64) - floor(o / 64) + 2 columns between o and o' = o + n.  So the
 // columns need no prefix sum over block counts; 32 lanes probe the offsets at
 // once to find b (one round for up to 32 sequences, two for 1024), and the
-// last round brings the run's end and position along.  Every thread of the
+// last round brings the run's end and position along.  (Offsets that decrease
+// are reported, and may hide columns of other sequences from the search: their
+// blocks are left out, never written twice.)  Every thread of the
 // CTA gets the same answer; false where the column has no work.  flag: this
 // thread reports what is wrong with the run.  rest: the rows behind the last
 // sequence are handed out as a run without blocks.

@@ -453,8 +453,10 @@ int attn_mla_project_out(const void *z, const void *u_v, void *o, int B, int H, 
  * k_stride / v_stride: elements from one token's row to the next (at least
  * H_kv * d, a multiple of 8 (bf16) or 4 (fp32)): rows may be columns of a
  * fused projection.  Rows whose position or block id is out of range are
- * skipped and flagged (ATTN_ERR_BAD_BLOCK); offsets that decrease or leave
- * [0, n_tokens] flag ATTN_ERR_BAD_SEQLEN, and those rows are skipped.
+ * skipped and flagged (ATTN_ERR_BAD_BLOCK).  Offsets that decrease or leave
+ * [0, n_tokens] flag ATTN_ERR_BAD_SEQLEN: the runs whose ends are wrong are not
+ * written, and of the others any block may be left out (each block of a run is
+ * written whole, codes and scale, or not at all).
  * Allocates nothing.
  */
 int kv_append_fp8_block(const void *k_new, const void *v_new, int64_t k_stride, int64_t v_stride,
