@@ -838,8 +838,10 @@ int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cac
     p.B = B; p.q_len = q_len; p.H_q = H_q; p.H_kv = H_kv; p.group = H_q / H_kv;
     p.max_blocks = max_blocks_per_seq; p.num_blocks = num_blocks;
     p.vis = vis;
-    p.timeout_ns = kDefaultTimeoutNs;
-    return cuda_status(launch_gqa_fp8_block(p, d, workspace, (cudaStream_t)stream));
+    take_force_timeout(&p.force_timeout, &p.timeout_ns);
+    FbEvents events;
+    take_profile_events(&events.start, &events.stop);
+    return cuda_status(launch_gqa_fp8_block(p, d, workspace, events, (cudaStream_t)stream));
 }
 
 int attn_decode_plan(const int32_t *seq_lens, int B, int units_per_seq, int window,

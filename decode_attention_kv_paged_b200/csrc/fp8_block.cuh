@@ -59,6 +59,7 @@ struct GqaFp8BlockParams {
     Visibility vis;               // of a single query; the kernels widen the window by q_len - 1
     int num_ctas;
     unsigned long long timeout_ns;
+    int force_timeout;            // testing: each CTA waits for something that never comes
     // filled by the launch: the query rows of a K/V head (group x q_len) in
     // chunks of chunk_rows; partials [2 num_ctas][columns][d] with what they
     // are relative to, the largest score, and the sum of weights relative to it
@@ -73,7 +74,12 @@ struct GqaFp8BlockParams {
 // Workspace of a launch over num_ctas CTAs with `rows` query rows per K/V head.
 int64_t fp8_block_workspace_bytes(int num_ctas, int rows, int d);
 
+// Events that a caller wants recorded around the main kernel (null: none).
+struct FbEvents {
+    cudaEvent_t start, stop;
+};
+
 cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &p, int d, void *workspace,
-                                 cudaStream_t stream);
+                                 const FbEvents &events, cudaStream_t stream);
 
 }  // namespace attn

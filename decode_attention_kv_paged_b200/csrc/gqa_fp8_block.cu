@@ -138,8 +138,8 @@ struct FbShared {
     uint64_t k_full[kFbMaxStages], k_empty[kFbMaxStages];
     uint64_t v_full[kFbMaxStages], v_empty[kFbMaxStages];
     uint64_t q_full[2], o_full[4], q_empty[2], s_full[2], mma_final;
-    uint64_t o_free[4], g_sync[2], s_free[2], p_full[4];
-    static constexpr int kBars = 4 * kFbMaxStages + 23;
+    uint64_t o_free[4], g_sync[2], s_free[2], p_full[4], unsignalled;
+    static constexpr int kBars = 4 * kFbMaxStages + 24;
     alignas(16) FbTile tile[kFbRing];
     alignas(16) FbPart part[kFbRing];
     // Per tile and block: K scale x softmax scale (log2 units), log2 of the V
@@ -732,7 +732,8 @@ gqa_fp8_block_kernel(const __grid_constant__ CUtensorMap tm_k,
         };
         int ks = 0, seg = -1;
         uint32_t k_par = 0;
-        for (int n = 0;; ++n) {
+        const bool go = !p.force_timeout || wait(&sh->unsignalled, 0);
+        for (int n = 0; go; ++n) {
             if (n >= 2 && !wait(&sh->s_free[n & 1], (uint32_t)((n / 2 - 1) & 1))) break;
             if (!wait(&sh->k_full[ks], k_par)) break;
             const FbTile at = sh->tile[n % kFbRing];
@@ -1345,7 +1346,7 @@ bool fb_make_map(CUtensorMap *m, const void *base, int D, uint64_t rows) {
 }
 
 template <int D, int NQ, bool G>
-cudaError_t fb_launch(const GqaFp8BlockParams &p, cudaStream_t stream) {
+cudaError_t fb_launch(const GqaFp8BlockParams &p, const FbEvents &events, cudaStream_t stream) {
     using C = FbCfg<D, NQ>;
     static PerDeviceFlag configured;
     cudaError_t e = configure_once_per_device(configured, [] {
@@ -1371,7 +1372,9 @@ cudaError_t fb_launch(const GqaFp8BlockParams &p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (events.start && (e = cudaEventRecord(events.start, stream)) != cudaSuccess) return e;
     e = cudaLaunchKernelEx(&cfg, gqa_fp8_block_kernel<D, NQ, G>, tk, tv, p);
+    if (e == cudaSuccess && events.stop) e = cudaEventRecord(events.stop, stream);
     if (e != cudaSuccess || p.whole_units || p.num_ctas == 1) return e;
     cfg.gridDim = dim3((unsigned)p.num_ctas - 1);
     cfg.blockDim = dim3(kFbJoinThreads);
@@ -1380,19 +1383,19 @@ cudaError_t fb_launch(const GqaFp8BlockParams &p, cudaStream_t stream) {
 }
 
 template <int D>
-cudaError_t fb_launch_d(const GqaFp8BlockParams &p, cudaStream_t s) {
+cudaError_t fb_launch_d(const GqaFp8BlockParams &p, const FbEvents &e, cudaStream_t s) {
     const bool g = p.vis.n_g > 0;
     switch (fb_columns(p.chunk_rows)) {
-        case 8: return g ? fb_launch<D, 8, true>(p, s) : fb_launch<D, 8, false>(p, s);
-        case 16: return g ? fb_launch<D, 16, true>(p, s) : fb_launch<D, 16, false>(p, s);
-        default: return g ? fb_launch<D, 32, true>(p, s) : fb_launch<D, 32, false>(p, s);
+        case 8: return g ? fb_launch<D, 8, true>(p, e, s) : fb_launch<D, 8, false>(p, e, s);
+        case 16: return g ? fb_launch<D, 16, true>(p, e, s) : fb_launch<D, 16, false>(p, e, s);
+        default: return g ? fb_launch<D, 32, true>(p, e, s) : fb_launch<D, 32, false>(p, e, s);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &given, int d, void *workspace,
-                                 cudaStream_t stream) {
+                                 const FbEvents &events, cudaStream_t stream) {
     GqaFp8BlockParams p = given;
     const int rows = p.group * p.q_len;
     p.chunk_rows = fp8_block_rows(rows);
@@ -1410,9 +1413,9 @@ cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &given, int d, void *wo
     p.small_plan = p.B <= 32 &&
                    (double)p.B * p.H_kv * p.chunks * p.max_blocks * (p.num_ctas + 1.0) < 4e9;
     switch (d) {
-        case 64: return fb_launch_d<64>(p, stream);
-        case 128: return fb_launch_d<128>(p, stream);
-        default: return fb_launch_d<256>(p, stream);
+        case 64: return fb_launch_d<64>(p, events, stream);
+        case 128: return fb_launch_d<128>(p, events, stream);
+        default: return fb_launch_d<256>(p, events, stream);
     }
 }
 

@@ -514,7 +514,9 @@ int kv_read_fp8_block(const void *k_cache, const void *v_cache, const float *k_s
  * bytes, 256-byte aligned, which nothing else uses until the call's work is
  * done (a captured graph keeps its own); its contents need no preparation.
  * ATTN_ERR_ARG if it is too small.  Allocates nothing.  Other errors as
- * attn_decode_gqa_ext.
+ * attn_decode_gqa_ext.  attn_set_num_ctas, attn_set_profile_events (around the
+ * main kernel, not the one that joins split units) and attn_debug_force_timeout
+ * apply.
  */
 int attn_decode_gqa_fp8_block(const void *q, int64_t q_stride, const void *k_cache,
                               const void *v_cache, const float *k_scale, const float *v_scale,
