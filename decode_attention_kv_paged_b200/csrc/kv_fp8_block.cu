@@ -64,6 +64,9 @@ __device__ __forceinline__ int named_slot(const Visibility &v, int b, int blk) {
 // goes there.  A writer goes there for the blocks that lie before the window
 // when the run is done (the decode then reads them there, and a run longer than
 // the ring replaces them itself), else through the ring like kv_append_ext.
+// G: the call has such a table (compiled out of the other kernels, which it
+// would cost 5 % of a ragged append's time: 14.4 against 13.7 us).
+template <bool G>
 __device__ __forceinline__ bool locate_run(const KvRunParams &p, int x, bool flag, bool rest,
                                            bool reading, BlockRun *out) {
     const int lane = threadIdx.x & 31;
@@ -125,8 +128,7 @@ __device__ __forceinline__ bool locate_run(const KvRunParams &p, int x, bool fla
     if (blk > last) return false;
     int slot = table_slot(p.vis, blk);
     bool replaced = p.vis.ring > 0 && slot >= ring_base(p.vis) && blk + p.vis.ring <= last;
-    if (p.vis.ring > 0 && p.vis.n_g > 0 &&
-        (reading || blk < window_lo(p.vis, pos + n) / kBlockSize)) {
+    if (G && (reading || blk < window_lo(p.vis, pos + n) / kBlockSize)) {
         const int named = named_slot(p.vis, b, blk);
         if (named >= 0) {
             slot = named;
@@ -226,7 +228,7 @@ template <> struct CodesOf<16> { using type = uint4; };
 // resident CTAs hold together count.  Measured: 256 MiB of fp32 rows of d = 64
 // 109 us (0.94 of the copy rate; 124 with 256 threads of 4 values), 107 MB of
 // bf16 rows of d = 64 32 us (0.76; 47 with 256 threads of 8 values).
-template <typename T, int D>
+template <typename T, int D, bool G>
 __global__ void __launch_bounds__(D, (sizeof(T) == 2 ? 1024 : 640) / D)
 kv_append_fp8_block_kernel(const KvAppendBlockParams p) {
     constexpr int kE = 16, kC = sizeof(T);                 // values, 16-byte chunks of them
@@ -239,7 +241,7 @@ kv_append_fp8_block_kernel(const KvAppendBlockParams p) {
     pdl_launch_dependents();
     BlockRun br;
     const bool flag = tid == 0 && h == 0 && !is_v;
-    if (!locate_run(p.run, blockIdx.x, flag, false, false, &br)) return;
+    if (!locate_run<G>(p.run, blockIdx.x, flag, false, false, &br)) return;
     const T *src = static_cast<const T *>(is_v ? p.v_new : p.k_new);
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
     const int col = (tid % kTpr) * kE, row0 = tid / kTpr;
@@ -326,7 +328,7 @@ __device__ __forceinline__ uint4 out_chunk(const float *f, float) {
 // A CTA reads 1 << heads_log2 heads of a block; a thread keeps to one head and
 // one 16-byte chunk of the output row, so that its scale stays in a register
 // and neighbours write neighbouring chunks.
-template <typename T, int D>
+template <typename T, int D, bool G>
 __global__ void __launch_bounds__(kRunThreads)
 kv_read_fp8_block_kernel(const KvReadBlockParams p, int heads_log2) {
     constexpr int kE = In<T>::kE, kTpr = D / kE, kUnits = kRunThreads / kTpr;
@@ -347,7 +349,7 @@ kv_read_fp8_block_kernel(const KvReadBlockParams p, int heads_log2) {
     }
     BlockRun br;
     const bool flag = tid == 0 && blockIdx.y == 0 && !is_v;
-    if (!locate_run(p.run, blockIdx.x, flag, p.zero_rest, true, &br)) return;
+    if (!locate_run<G>(p.run, blockIdx.x, flag, p.zero_rest, true, &br)) return;
     const int phys = run_block(p.run, br, flag, true);
     dst += ((int64_t)br.src - br.r0) * (int64_t)pitch;
     if (phys < 0) {
@@ -400,17 +402,24 @@ cudaError_t launch_run(K kernel, dim3 grid, int threads, cudaStream_t stream, A.
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename T>
+// A ring with a global set: see locate_run.
+bool has_global_slots(const Visibility &v) { return v.ring > 0 && v.n_g > 0; }
+
+template <typename T, bool G>
 cudaError_t append_d(const KvAppendBlockParams &p, int d, cudaStream_t s) {
     const dim3 g(run_columns(p.run, false), (unsigned)p.run.H_kv, 2u);
     switch (d) {
-        case 64: return launch_run(kv_append_fp8_block_kernel<T, 64>, g, 64, s, p);
-        case 128: return launch_run(kv_append_fp8_block_kernel<T, 128>, g, 128, s, p);
-        default: return launch_run(kv_append_fp8_block_kernel<T, 256>, g, 256, s, p);
+        case 64: return launch_run(kv_append_fp8_block_kernel<T, 64, G>, g, 64, s, p);
+        case 128: return launch_run(kv_append_fp8_block_kernel<T, 128, G>, g, 128, s, p);
+        default: return launch_run(kv_append_fp8_block_kernel<T, 256, G>, g, 256, s, p);
     }
 }
-
 template <typename T>
+cudaError_t append_t(const KvAppendBlockParams &p, int d, cudaStream_t s) {
+    return has_global_slots(p.run.vis) ? append_d<T, true>(p, d, s) : append_d<T, false>(p, d, s);
+}
+
+template <typename T, bool G>
 cudaError_t read_d(const KvReadBlockParams &p, int d, cudaStream_t s) {
     // Heads of a CTA: the largest power of two that divides them, up to 32 KB
     // of codes, so that finding the rows is paid once for many.
@@ -418,22 +427,26 @@ cudaError_t read_d(const KvReadBlockParams &p, int d, cudaStream_t s) {
     while ((2 << lg) * kBlockSize * d <= 32768 && p.run.H_kv % (2 << lg) == 0) ++lg;
     const dim3 g(run_columns(p.run, p.zero_rest), (unsigned)(p.run.H_kv >> lg), 2u);
     switch (d) {
-        case 64: return launch_run(kv_read_fp8_block_kernel<T, 64>, g, kRunThreads, s, p, lg);
-        case 128: return launch_run(kv_read_fp8_block_kernel<T, 128>, g, kRunThreads, s, p, lg);
-        default: return launch_run(kv_read_fp8_block_kernel<T, 256>, g, kRunThreads, s, p, lg);
+        case 64: return launch_run(kv_read_fp8_block_kernel<T, 64, G>, g, kRunThreads, s, p, lg);
+        case 128: return launch_run(kv_read_fp8_block_kernel<T, 128, G>, g, kRunThreads, s, p, lg);
+        default: return launch_run(kv_read_fp8_block_kernel<T, 256, G>, g, kRunThreads, s, p, lg);
     }
+}
+template <typename T>
+cudaError_t read_t(const KvReadBlockParams &p, int d, cudaStream_t s) {
+    return has_global_slots(p.run.vis) ? read_d<T, true>(p, d, s) : read_d<T, false>(p, d, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append_fp8_block(const KvAppendBlockParams &p, int d, bool bf16,
                                        cudaStream_t stream) {
-    return bf16 ? append_d<__nv_bfloat16>(p, d, stream) : append_d<float>(p, d, stream);
+    return bf16 ? append_t<__nv_bfloat16>(p, d, stream) : append_t<float>(p, d, stream);
 }
 
 cudaError_t launch_kv_read_fp8_block(const KvReadBlockParams &p, int d, bool bf16,
                                      cudaStream_t stream) {
-    return bf16 ? read_d<__nv_bfloat16>(p, d, stream) : read_d<float>(p, d, stream);
+    return bf16 ? read_t<__nv_bfloat16>(p, d, stream) : read_t<float>(p, d, stream);
 }
 
 }  // namespace attn
