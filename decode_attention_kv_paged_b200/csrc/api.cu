@@ -452,7 +452,11 @@ int attn_decode_gqa(const void *q, const void *k_cache, const void *v_cache,
 static int check_visibility(const attn_visibility *v, int max_blocks_per_seq, Visibility *out) {
     if (!v) return ATTN_ERR_ARG;
     if (v->sink_tokens < 0 || v->ring_blocks < 0 || v->n_global < 0) return ATTN_ERR_ARG;
-    Visibility vis{v->window > 0 ? v->window : 0, v->sink_tokens, v->ring_blocks};
+    // A prefix within a block of what an int counts would wrap around when it is
+    // rounded up to blocks; no position lies that far out.
+    constexpr int kMaxSink = (1 << 30) - 1 + (1 << 30) - kBlockSize;
+    Visibility vis{v->window > 0 ? v->window : 0,
+                   v->sink_tokens < kMaxSink ? v->sink_tokens : kMaxSink, v->ring_blocks};
     if (v->n_global > 0) {
         // An explicit global set replaces the sink prefix; with a ring its
         // positions' blocks keep the n_global slots ahead of the ring.
