@@ -3,9 +3,20 @@
 // its append, read-back and decode kernels.
 #pragma once
 
+#include <cuda.h>
+
 #include "plan.cuh"
 
 namespace attn {
+
+// The driver's tensor-map encoder (null where it cannot be had), looked up
+// once by gqa_tc.cu.
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                   CUtensorMapFloatOOBfill);
+EncodeTiledFn tc_encode_fn();
 
 struct KvRunParams {
     const int32_t *positions;     // [B] first position of sequence b's run

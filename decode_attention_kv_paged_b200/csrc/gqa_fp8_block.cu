@@ -61,7 +61,6 @@
 #include <cuda_fp8.h>
 
 #include "fp8_block.cuh"
-#include "gqa_tc.cuh"
 #include "host_state.cuh"
 #include "tc_common.cuh"
 

@@ -37,14 +37,6 @@ bool gqa_tc128_fp8_supported(int d, int G);
 int gqa_tc128_fp8_heads_per_cta(int G);
 cudaError_t launch_gqa_tc128_fp8(const GqaLaunch &L, int d, int HC);
 
-// The driver's tensor-map encoder (null where it cannot be had).
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-EncodeTiledFn tc_encode_fn();
-
 // 2-D tensor map over a row-major bf16 matrix [rows][cols] with 64-column,
 // box_rows-row boxes and 128-byte swizzle.
 bool tc_make_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows,
