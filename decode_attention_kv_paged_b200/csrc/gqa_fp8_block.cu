@@ -232,8 +232,8 @@ __device__ __forceinline__ void umma_commit_by(uint32_t lead, uint64_t *bar) {
 
 template <int N>
 __device__ __forceinline__ void fb_tmem_ld(uint32_t addr, float *v) {
-    if constexpr (N == 64) tmem_ld64(addr, v);
-    else if constexpr (N == 32) tmem_ld32(addr, v);
+    static_assert(N == 16 || N == 32, "columns of a load");
+    if constexpr (N == 32) tmem_ld32(addr, v);
     else tmem_ld16(addr, v);
 }
 

@@ -186,9 +186,6 @@ __device__ __forceinline__ uint32_t four_codes(const float *f, float by) {
                                                  __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
 }
-__device__ __forceinline__ void to_codes(const float *f, float by, uint2 *c) {
-    *c = make_uint2(four_codes(f, by), four_codes(f + 4, by));
-}
 __device__ __forceinline__ void to_codes(const float *f, float by, uint4 *c) {
     *c = make_uint4(four_codes(f, by), four_codes(f + 4, by), four_codes(f + 8, by),
                     four_codes(f + 12, by));
