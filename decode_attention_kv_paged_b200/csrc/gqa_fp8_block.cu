@@ -50,13 +50,19 @@
 // first by programmatic launch, joins: one CTA per cut, splits in order.
 //
 // What bounds it (device time; floor: codes once at the copy rate).  32 heads
-// of their own, 8 x 32768 tokens, d = 128: 332 us, 0.99 of the copy rate.  One
-// K/V head for 32 query heads: the softmax, 1.2 us a tile against 0.74 for its
-// bytes.  Middling sizes (16 x 4096 tokens, 8 K/V heads: 35 us, floor 20.5):
-// some 4 us until the first tile is there (lengths, table and codes are loads
-// that wait for one another) and 4 us for the second kernel.  The instruction
-// cache mattered as much as anything: no warp's loop may be long, so records
-// replace walks over the work list, and slow paths are out of line.
+// of their own, 8 x 32768 tokens, d = 128: 336 us, 0.98 of the copy rate, for
+// the first 50 ms; a loop that goes on reaches the 1000 W cap, the SM clock
+// falls from 1965 to 1690 MHz, and it takes 346 to 386 us on different devices.
+// Up to 8 columns a tile of 128 keys costs its bytes (0.74 us at d = 128).
+// With 32 columns it is the softmax, 1.44 us a tile whether 20 or 32 rows are
+// used: both groups work on one tile, some 2900 cycles from one to the next.
+// Beside the tiles a call takes 14 us with up to 8 columns, 18 with d = 256, 24
+// with 32 (fits over lengths): the first K tile is there after 4.0 us (lengths,
+// table and codes are loads that wait for one another), its weights after 6.0,
+// then come the uneven ends of the CTAs and the second kernel (16 x 4096 tokens,
+// 8 K/V heads: 34.7 us, floor 20.5).  The instruction cache mattered as much as
+// anything: no warp's loop may be long, so records replace walks over the work
+// list, and slow paths are out of line.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -1404,9 +1410,13 @@ cudaError_t launch_gqa_fp8_block(const GqaFp8BlockParams &given, int d, void *wo
     p.ws_o = reinterpret_cast<float *>(p.ws_cut + kFp8BlockMaxCtas);
     p.ws_ml = reinterpret_cast<float4 *>(p.ws_o + slots * d);
     // Where no sequence can be long and there is an SM for every unit, a unit
-    // is not split: that saves the plan and the second kernel.  Measured with
-    // 32 units of 4 rows, d = 128: 8.5 us against 20.6 at 512 tokens, 16.5
-    // against 21.6 at 2048, 27.4 against 23.2 at 4096.
+    // is not split: that saves the plan and the second kernel.  The lengths are
+    // on the device, so the table's width decides: a wider table takes the split
+    // whatever its sequences hold.  Measured, whole against split, d = 128: 32
+    // units of 4 rows 8.8 us against 16.3 at 512 tokens, 11.8 against 17.0 at
+    // 1024, 17.3 against 17.6 at 2048; 128 units 10.3 against 17.9 and 18.4
+    // against 24.5 at 512 and 2048; one unit of 32 rows 12.8 against 15.7 at 512,
+    // but 30.2 against 21.3 at 2048.
     p.whole_units = p.max_blocks <= kFbWholeBlocks &&
                     (long long)p.B * p.H_kv * p.chunks <= p.num_ctas;
     p.small_plan = p.B <= 32 &&

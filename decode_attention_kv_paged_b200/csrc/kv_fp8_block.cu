@@ -5,7 +5,7 @@
 // one CTA sees every new row of the block, holds them in registers between
 // finding the maximum and writing the codes, and reads each input once.
 // Read-back: one CTA per (block, up to 8 heads, K or V), 16-byte stores; 128 MiB
-// of codes to bf16 take 69 us, 0.88 of the copy rate (152 us with one head a CTA
+// of codes to bf16 take 70 us, 0.88 of the copy rate (152 us with one head a CTA
 // and a thread's 16 values in two stores).
 // Both are bound by memory; what is left beside that is the chain of dependent
 // loads that finds a CTA its rows (offsets and positions, block table, data).
@@ -223,7 +223,7 @@ template <> struct CodesOf<16> { using type = uint4; };
 // threads with much in flight each: what bounds the kernel beside HBM is the
 // time of a CTA (three loads that wait for one another), so the bytes that all
 // resident CTAs hold together count.  Measured: 256 MiB of fp32 rows of d = 64
-// 109 us (0.94 of the copy rate; 124 with 256 threads of 4 values), 107 MB of
+// 106 to 109 us (0.94 to 0.97 of the copy rate; 124 with 256 threads of 4 values), 107 MB of
 // bf16 rows of d = 64 32 us (0.76; 47 with 256 threads of 8 values).
 template <typename T, int D, bool G>
 __global__ void __launch_bounds__(D, (sizeof(T) == 2 ? 1024 : 640) / D)
