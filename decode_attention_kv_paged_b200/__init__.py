@@ -521,7 +521,8 @@ def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scale, v_scale, positi
     position positions[b] of sequence b on; without offsets row b is sequence
     b's.  A block whose first row is written takes the scale its rows ask for;
     a block begun earlier keeps its scale or grows it, its codes rounded to the
-    new one."""
+    new one.  In a ring table with global_pos, a run's blocks that hold a global
+    position and lie before the window at its end go to their global slots."""
     dev, handle, where = _place(k_new, "k_new", stream)
     if where is None:
         return _append_fp8_block(dev, handle, k_new, v_new, k_cache, v_cache, k_scale, v_scale,
@@ -564,6 +565,8 @@ def kv_read_fp8_block(k_cache, v_cache, k_scale, v_scale, positions, block_table
     """(k, v) [n_tokens][H_kv][d]: cached rows read back, code value times block
     scale rounded to `dtype` (bf16 or fp32).  Row offsets[b] + t is position
     positions[b] + t of sequence b; without offsets row b is positions[b].
+    In a ring table, blocks that hold a position of global_pos are read from
+    their global slots; other positions have to be ones that the ring still holds.
     `out`: a pair to write into, whose rows behind offsets[B] are left as they
     were; in new tensors they are zeros."""
     dev, handle, where = _place(k_cache, "k_cache", stream)
